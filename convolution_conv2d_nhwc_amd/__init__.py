@@ -16,4 +16,7 @@ def __getattr__(name):
                 "conv_out_shape", "pack_bias_scale"):
         from . import _lib
         return getattr(_lib, name)
+    if name in ("group_norm", "group_norm_grad", "head_loss", "head_loss_grad", "orthogonalize"):
+        from . import train
+        return getattr(train, name)
     raise AttributeError(name)

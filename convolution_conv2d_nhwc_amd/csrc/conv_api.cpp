@@ -17,6 +17,7 @@
 
 #include "device_common.h"
 #include "plan.h"
+#include "train.h"
 
 using namespace convnhwc;
 
@@ -156,13 +157,23 @@ conv_status plan_split_k(conv_plan* p, void* scratch, int64_t scratch_bytes) {
   return CONV_OK;
 }
 
+}  // namespace
+
+namespace convnhwc {
+
 bool ranges_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   if (!a || !b || na <= 0 || nb <= 0) return false;
   const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
   return a0 < b0 + (uintptr_t)nb && b0 < a0 + (uintptr_t)na;
 }
 
-}  // namespace
+conv_status hip_status(hipError_t err) {
+  if (err == hipSuccess) return CONV_OK;
+  std::snprintf(g_last_hip_error, sizeof(g_last_hip_error), "%s", hipGetErrorString(err));
+  return CONV_E_HIP;
+}
+
+}  // namespace convnhwc
 
 namespace {
 
@@ -783,7 +794,7 @@ const char* conv_status_str(int32_t status) {
     case CONV_E_NOMEM: return "CONV_E_NOMEM: plan or split-K workspace allocation failed";
     case CONV_E_SCRATCH:
       return "CONV_E_SCRATCH: the layer's split-K partial sums exceed the static scratch of conv_run_noalloc "
-             "(CONV_NOALLOC_SCRATCH_BYTES)";
+             "(CONV_NOALLOC_SCRATCH_BYTES), or a training-side operator's ws is too small";
     case CONV_E_HIP:
       std::snprintf(buf, sizeof(buf), "CONV_E_HIP: %s", g_last_hip_error);
       return buf;

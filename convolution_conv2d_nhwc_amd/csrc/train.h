@@ -1,0 +1,56 @@
+// train.h -- internal declarations of the training-side operators
+// (include/conv_train.h): plans computed on the host, kernel launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/conv_train.h"
+
+namespace convnhwc {
+
+// Keeps the text of a HIP error for conv_status_str; CONV_OK for hipSuccess.
+conv_status hip_status(hipError_t err);
+bool ranges_overlap(const void* a, int64_t an, const void* b, int64_t bn);
+
+// ---- group norm ---------------------------------------------------------------
+
+// How a (n, h*w, c) map is cut: channel tiles of whole groups (tpg == 1) or
+// parts of one group (gpt == 1, tpg > 1), pixel chunks of ppi * r pixels.
+struct NormPlan {
+  int vec;     // elements per load
+  int ct;      // channels per tile (a multiple of vec)
+  int gpt;     // groups per tile
+  int tpg;     // tiles per group
+  int ctiles;  // channel tiles
+  int ppi;     // pixels a workgroup covers per step
+  int r;       // steps kept in registers
+  int chunks;  // pixel chunks per image (1 with tpg == 1: one launch)
+};
+
+struct NormArgs {
+  const void* x;
+  const void* dy;
+  const float* gamma;
+  const float* beta;
+  void* y;       // y, or dx of the gradient
+  float* stats;  // [n][groups][2]: written by the forward pass when not null, read by the gradient
+  float* part;   // ws: forward [n][groups][chunks * tpg][2]; gradient [n][chunks][c][2]
+  float* tot;    // ws: gradient [n][c][2] per-image channel sums
+  float* means;  // ws: gradient [n][groups][2]
+  float* dgamma;
+  float* dbeta;
+  int64_t pitch;  // elements per pixel of x
+  int n, hw, c, groups, cg;
+  float eps, inv_count;
+  int act;
+  NormPlan p;
+};
+
+// align: the byte alignment that x, dy and y share (a power of two, at most 16).
+NormPlan norm_plan(const conv_norm_desc& d, bool grad, int align);
+int64_t norm_ws_bytes(const conv_norm_desc& d, const NormPlan& p, bool grad);
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s);
+hipError_t launch_norm_grad(const NormArgs& a, int dtype, hipStream_t s);
+
+}  // namespace convnhwc

@@ -1,0 +1,152 @@
+// train_api.cpp -- C entry points of the training-side operators
+// (include/conv_train.h): argument checks on the host, then the launchers.
+#include <algorithm>
+#include <cmath>
+
+#include "train.h"
+
+using namespace convnhwc;
+
+namespace {
+
+constexpr int64_t kMaxBytes = (int64_t)1 << 31;
+
+// The byte alignment an address has, up to 16 (16 for NULL).
+int align_of(const void* p) {
+  const uintptr_t v = (uintptr_t)p;
+  return v & 15 ? (int)(v & (~v + 1)) : 16;
+}
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+
+// Whether any output overlaps an input or another output.
+template <int NI, int NO>
+bool aliased(const Range (&in)[NI], const Range (&out)[NO]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < NI; ++j)
+      if (ranges_overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return true;
+    for (int j = 0; j < i; ++j)
+      if (ranges_overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+  }
+  return false;
+}
+
+// ---- group norm ---------------------------------------------------------------
+
+conv_status norm_check(const conv_norm_desc* d) {
+  if (!d) return CONV_E_NULL;
+  if (d->n <= 0 || d->h <= 0 || d->w <= 0 || d->c <= 0 || d->groups <= 0 || d->c % d->groups ||
+      d->x_pixel_stride < 0 || (d->x_pixel_stride && d->x_pixel_stride < d->c) || !(d->eps >= 0.0f) ||
+      !std::isfinite(d->eps))
+    return CONV_E_SHAPE;
+  if (d->dtype != CONV_F32 && d->dtype != CONV_BF16) return CONV_E_UNSUPPORTED;
+  if (d->act < CONV_ACT_NONE || d->act > CONV_ACT_SILU) return CONV_E_UNSUPPORTED;
+  const int64_t esz = d->dtype == CONV_F32 ? 4 : 2, pitch = d->x_pixel_stride ? d->x_pixel_stride : d->c;
+  // each factor bounded before the product, so that it cannot wrap
+  if (d->n > 65535 || d->h >= kMaxBytes || d->w >= kMaxBytes || pitch >= kMaxBytes) return CONV_E_UNSUPPORTED;
+  if (d->h * d->w >= kMaxBytes || d->h * d->w * d->n >= kMaxBytes ||
+      (double)d->h * d->w * d->n * pitch * esz >= (double)kMaxBytes)
+    return CONV_E_UNSUPPORTED;
+  // channel tiles are a grid dimension
+  if (d->c > 65535) return CONV_E_UNSUPPORTED;
+  return CONV_OK;
+}
+
+// Scratch that is enough whatever the pointers' alignment.
+int64_t norm_ws(const conv_norm_desc& d, bool grad) {
+  int64_t most = 0;
+  for (int align = 2; align <= 16; align *= 2)
+    most = std::max(most, norm_ws_bytes(d, norm_plan(d, grad, align), grad));
+  return most;
+}
+
+NormArgs norm_args(const conv_norm_desc& d) {
+  NormArgs a = {};
+  a.pitch = d.x_pixel_stride ? d.x_pixel_stride : d.c;
+  a.n = (int)d.n;
+  a.hw = (int)(d.h * d.w);
+  a.c = (int)d.c;
+  a.groups = d.groups;
+  a.cg = (int)(d.c / d.groups);
+  a.eps = d.eps;
+  a.inv_count = (float)(1.0 / ((double)a.hw * a.cg));
+  a.act = d.act;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t conv_group_norm_ws_bytes(const conv_norm_desc* d, int32_t grad) {
+  const conv_status st = norm_check(d);
+  if (st != CONV_OK) return st;
+  const int64_t b = norm_ws(*d, grad != 0);
+  return b >= kMaxBytes ? (int64_t)CONV_E_UNSUPPORTED : b;
+}
+
+conv_status conv_group_norm(const conv_norm_desc* d, const void* x, const float* gamma, const float* beta, void* y,
+                            float* stats, void* ws, int64_t ws_bytes, void* stream) {
+  if (!d || !x || !y) return CONV_E_NULL;
+  const int64_t need = conv_group_norm_ws_bytes(d, 0);
+  if (need < 0) return (conv_status)need;
+  const int esz = d->dtype == CONV_F32 ? 4 : 2;
+  if (((uintptr_t)x | (uintptr_t)y) & (esz - 1)) return CONV_E_ALIGN;
+  if (((uintptr_t)gamma | (uintptr_t)beta | (uintptr_t)stats) & 3) return CONV_E_ALIGN;
+  if (need > 0 && !ws) return CONV_E_NULL;
+  if ((uintptr_t)ws & 255) return CONV_E_ALIGN;
+  if (need > ws_bytes) return CONV_E_SCRATCH;
+  NormArgs a = norm_args(*d);
+  const int64_t px = d->n * a.hw;
+  const Range in[] = {{x, ((px - 1) * a.pitch + a.c) * esz}, {gamma, a.c * 4}, {beta, a.c * 4}};
+  const Range out[] = {{y, px * a.c * esz}, {stats, (int64_t)a.n * a.groups * 8}, {ws, need}};
+  if (aliased(in, out)) return CONV_E_ALIAS;
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.y = y;
+  a.stats = stats;
+  a.part = static_cast<float*>(ws);
+  a.p = norm_plan(*d, false, std::min(align_of(x), align_of(y)));
+  return hip_status(launch_norm(a, d->dtype, static_cast<hipStream_t>(stream)));
+}
+
+conv_status conv_group_norm_grad(const conv_norm_desc* d, const void* x, const void* dy, const float* stats,
+                                 const float* gamma, const float* beta, void* dx, float* dgamma, float* dbeta,
+                                 void* ws, int64_t ws_bytes, void* stream) {
+  if (!d || !x || !dy || !stats || !dx) return CONV_E_NULL;
+  const int64_t need = conv_group_norm_ws_bytes(d, 1);
+  if (need < 0) return (conv_status)need;
+  const int esz = d->dtype == CONV_F32 ? 4 : 2;
+  if (((uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx) & (esz - 1)) return CONV_E_ALIGN;
+  if (((uintptr_t)gamma | (uintptr_t)beta | (uintptr_t)stats | (uintptr_t)dgamma | (uintptr_t)dbeta) & 3)
+    return CONV_E_ALIGN;
+  if (need > 0 && !ws) return CONV_E_NULL;
+  if ((uintptr_t)ws & 255) return CONV_E_ALIGN;
+  if (need > ws_bytes) return CONV_E_SCRATCH;
+  NormArgs a = norm_args(*d);
+  const int64_t px = d->n * a.hw, st_bytes = (int64_t)a.n * a.groups * 8;
+  const Range in[] = {{x, ((px - 1) * a.pitch + a.c) * esz}, {dy, px * a.c * esz}, {stats, st_bytes},
+                      {gamma, a.c * 4}, {beta, a.c * 4}};
+  const Range out[] = {{dx, px * a.c * esz}, {dgamma, a.c * 4}, {dbeta, a.c * 4}, {ws, need}};
+  if (aliased(in, out)) return CONV_E_ALIAS;
+  a.x = x;
+  a.dy = dy;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.y = dx;
+  a.stats = const_cast<float*>(stats);
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.p = norm_plan(*d, true, std::min(align_of(x), std::min(align_of(dy), align_of(dx))));
+  // ws: [n][c][2] totals, [n][groups][2] means, [n][chunks][c][2] chunk sums
+  a.tot = static_cast<float*>(ws);
+  a.means = a.tot + 2 * d->n * d->c;
+  a.part = a.means + 2 * d->n * d->groups;
+  return hip_status(launch_norm_grad(a, d->dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,84 @@
+/*
+ * conv_train.h -- C ABI of the training-side operators that stand next to
+ * the convolutions of conv_nhwc.h, for fitting a head on the maps a stack of
+ * layers produces: group norm with its activation over NHWC maps (forward
+ * and gradients), the softmax cross entropy of a 1x1 head over a large set
+ * of classes (forward and gradients) and the orthogonalised update of weight
+ * matrices.
+ *
+ * Conventions as in conv_nhwc.h: device buffers are owned by the caller, an
+ * entry point validates on the host, returns a negative conv_status without
+ * enqueueing anything when it refuses, and otherwise only enqueues kernels
+ * on the given stream (no allocation, no synchronisation, nothing cached
+ * between calls, no memset node), so every call can be captured into a HIP
+ * graph. A call that needs scratch memory takes it as `ws` (256-byte
+ * aligned); the *_ws_bytes function of the operator gives its size, 0 when
+ * none is needed (ws may then be NULL), or a negative conv_status for a
+ * description the operator refuses. ws holds nothing between calls; calls
+ * that may run at the same time need a ws each. Too small a ws is
+ * CONV_E_SCRATCH. Every result is the same on every run: no atomic adds.
+ * An output overlapping an input, another output or ws is CONV_E_ALIAS.
+ * Each tensor and ws must be smaller than 2^31 bytes (CONV_E_UNSUPPORTED).
+ */
+#ifndef CONV_TRAIN_H
+#define CONV_TRAIN_H
+
+#include "conv_nhwc.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Activations of the norm: those of conv_act, and SiLU(v) = v / (1 + e^-v). */
+enum { CONV_ACT_SILU = 4 };
+
+/* Group norm over an NHWC map, then an activation:
+ *   mean, var over the h * w * (c / groups) values of (image, group),
+ *   xhat = (x - mean) / sqrt(var + eps)        (var the biased variance)
+ *   y    = act(gamma[ch] * xhat + beta[ch]). */
+typedef struct conv_norm_desc {
+  int64_t n, h, w, c;
+  int64_t x_pixel_stride; /* elements from one pixel of x to the next, >= c; 0 = c. A
+                             channel slice of a wider map is read in place. */
+  int32_t groups;         /* divides c */
+  int32_t dtype;          /* of x, y, dy, dx: CONV_F32 or CONV_BF16 (one RNE
+                             rounding; all arithmetic and sums in fp32) */
+  int32_t act;            /* conv_act or CONV_ACT_SILU */
+  float eps;              /* >= 0, finite */
+} conv_norm_desc;
+
+/* Scratch of conv_group_norm (grad = 0) or conv_group_norm_grad (grad = 1). */
+int64_t conv_group_norm_ws_bytes(const conv_norm_desc* d, int32_t grad);
+
+/*   x           : device [n][h][w] pixels x_pixel_stride elements apart
+ *   gamma, beta : device float[c], or NULL for 1 and 0
+ *   y           : device [n][h][w][c] of dtype
+ *   stats       : device float[n][groups][2], receives (mean, 1/sqrt(var + eps))
+ *                 for the gradients, or NULL
+ * Pointers aligned to their element (16-byte aligned x and y with c and
+ * x_pixel_stride whole 16-byte chunks run fastest), ws to 256 bytes.
+ * CONV_E_SHAPE: a size or groups <= 0, c not divisible by groups,
+ * x_pixel_stride < c, eps negative or not finite. CONV_E_UNSUPPORTED: dtype,
+ * act, n > 65535 or a size limit. */
+conv_status conv_group_norm(const conv_norm_desc* d, const void* x, const float* gamma, const float* beta, void* y,
+                            float* stats, void* ws, int64_t ws_bytes, void* stream);
+
+/* Gradients of conv_group_norm for the upstream gradient dy, from its x,
+ * stats, gamma and beta:
+ *   dz = dy * act'(z), z = gamma * xhat + beta,
+ *   dbeta[ch] = sum dz, dgamma[ch] = sum dz * xhat  over images and pixels,
+ *   dx = rstd * (gamma dz - m1 - xhat m2), m1 and m2 the means of gamma dz and
+ *        gamma dz xhat over the (image, group).
+ * act' of ReLU is 1 for z > 0, of ReLU6 1 for 0 < z < 6, else 0.
+ *   dy, dx        : device [n][h][w][c] of dtype
+ *   dgamma, dbeta : device float[c], either may be NULL
+ * Errors as conv_group_norm. */
+conv_status conv_group_norm_grad(const conv_norm_desc* d, const void* x, const void* dy, const float* stats,
+                                 const float* gamma, const float* beta, void* dx, float* dgamma, float* dbeta,
+                                 void* ws, int64_t ws_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* CONV_TRAIN_H */
