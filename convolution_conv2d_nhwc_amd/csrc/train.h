@@ -53,4 +53,60 @@ int64_t norm_ws_bytes(const conv_norm_desc& d, const NormPlan& p, bool grad);
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s);
 hipError_t launch_norm_grad(const NormArgs& a, int dtype, hipStream_t s);
 
+// ---- head loss ----------------------------------------------------------------
+
+// A product's tile side and the splits of its reduction.
+struct GemmShape {
+  int tile, splits;
+};
+
+// Tiles, pieces and the layout of ws (byte offsets; -1: not used).
+struct HeadPlan {
+  int64_t cpad;    // channels of the copies, a multiple of 8
+  int64_t rpad;    // row pitch of the transposed copies, a multiple of 64
+  int64_t vpad;    // class pitch of the transposed weights, a multiple of 64
+  int64_t cq;      // pitch of the fp32 partial sums, a multiple of 4
+  int64_t vp;      // classes per piece of the gradient, a multiple of 256
+  int slots;       // (max, sum) pairs per row
+  int stat_tile, ds_tile;
+  GemmShape dx, dw;
+  int64_t o_stat, o_lab, o_lse, o_scale;                       // forward
+  int64_t o_x, o_w, o_xt, o_wt, o_ds, o_dst, o_dxp, o_dwp;     // copies and gradient
+  int64_t bytes;
+};
+
+struct HeadArgs {
+  const uint16_t* x;
+  const uint16_t* w;
+  const void* labels;
+  const float* weights;
+  float* loss;
+  float* total;
+  uint16_t* dx;
+  uint16_t* dw;
+  char* ws;
+  int64_t rows, c, classes;
+  int label_bytes;
+  HeadPlan p;
+};
+
+// copy_x, copy_w: the operand cannot be read in place (c % 8 or alignment).
+HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w);
+hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s);
+
+// ---- orthogonalisation ----------------------------------------------------------
+
+struct OrthoArgs {
+  const void* g;
+  uint16_t* out;
+  char* ws;
+  int batch, rows, cols;
+  int steps;
+  float a, b, c, eps;
+  int g_f32;
+};
+
+int64_t ortho_ws_bytes(const conv_ortho_desc& d);
+hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s);
+
 }  // namespace convnhwc

@@ -77,9 +77,123 @@ NormArgs norm_args(const conv_norm_desc& d) {
   return a;
 }
 
+// ---- head loss ----------------------------------------------------------------
+
+conv_status head_check(const conv_head_desc* d) {
+  if (!d) return CONV_E_NULL;
+  if (d->rows <= 0 || d->c <= 0 || d->classes <= 0) return CONV_E_SHAPE;
+  if (d->dtype != CONV_BF16 || (d->label_bytes != 4 && d->label_bytes != 8)) return CONV_E_UNSUPPORTED;
+  // below 2^22 - 64 rows and classes the copies' grids (64 a workgroup) and the
+  // smallest piece of the gradient (256 classes by rows) stay in range
+  if (d->c > 65536 || d->rows > (1 << 22) - 64 || d->classes > (1 << 22) - 64) return CONV_E_UNSUPPORTED;
+  const int64_t c = (d->c + 7) / 8 * 8, most = (std::max(d->rows, d->classes) + 63) / 64 * 64;
+  if (most * c * 2 >= kMaxBytes) return CONV_E_UNSUPPORTED;
+  return CONV_OK;
+}
+
+conv_status head_run(const conv_head_desc* d, const void* x, const void* w, const void* labels, const float* weights,
+                     float* loss, float* total, void* dx, void* dw, void* ws, int64_t ws_bytes, void* stream,
+                     bool grad) {
+  if (!d || !x || !w || !labels || !loss || !total || (grad && (!dx || !dw))) return CONV_E_NULL;
+  const conv_status st = head_check(d);
+  if (st != CONV_OK) return st;
+  if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)dx | (uintptr_t)dw) & 1) return CONV_E_ALIGN;
+  if ((uintptr_t)labels & (d->label_bytes - 1)) return CONV_E_ALIGN;
+  if (((uintptr_t)weights | (uintptr_t)loss | (uintptr_t)total) & 3) return CONV_E_ALIGN;
+  if (!ws) return CONV_E_NULL;
+  if ((uintptr_t)ws & 255) return CONV_E_ALIGN;
+  HeadArgs a = {};
+  a.p = head_plan(*d, grad, d->c % 8 || ((uintptr_t)x & 15), d->c % 8 || ((uintptr_t)w & 15));
+  if (a.p.bytes > ws_bytes) return CONV_E_SCRATCH;
+  const int64_t xb = d->rows * d->c * 2, wb = d->classes * d->c * 2;
+  const Range in[] = {{x, xb}, {w, wb}, {labels, d->rows * d->label_bytes}, {weights, d->rows * 4}};
+  const Range out[] = {{loss, d->rows * 4}, {total, 4}, {dx, xb}, {dw, wb}, {ws, a.p.bytes}};
+  if (aliased(in, out)) return CONV_E_ALIAS;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = static_cast<const uint16_t*>(w);
+  a.labels = labels;
+  a.weights = weights;
+  a.loss = loss;
+  a.total = total;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dw = static_cast<uint16_t*>(dw);
+  a.ws = static_cast<char*>(ws);
+  a.rows = d->rows;
+  a.c = d->c;
+  a.classes = d->classes;
+  a.label_bytes = d->label_bytes;
+  return hip_status(launch_head_loss(a, grad, static_cast<hipStream_t>(stream)));
+}
+
+// ---- orthogonalisation ----------------------------------------------------------
+
+conv_status ortho_check(const conv_ortho_desc* d) {
+  if (!d) return CONV_E_NULL;
+  if (d->batch <= 0 || d->rows <= 0 || d->cols <= 0 || d->steps < 1 || d->steps > 100 || !std::isfinite(d->a) ||
+      !std::isfinite(d->b) || !std::isfinite(d->c) || !(d->eps >= 0.0f) || !std::isfinite(d->eps))
+    return CONV_E_SHAPE;
+  if (d->dtype != CONV_F32 && d->dtype != CONV_BF16) return CONV_E_UNSUPPORTED;
+  if (d->batch > 65535 || d->rows > 32768 || d->cols > 32768) return CONV_E_UNSUPPORTED;
+  const int64_t esz = d->dtype == CONV_F32 ? 4 : 2;
+  const int64_t rp = (d->rows + 63) / 64 * 64, cp = (d->cols + 63) / 64 * 64;
+  // one padded matrix is a product's operand; g is a tensor of its own
+  if (rp * cp * 2 >= kMaxBytes || d->batch * d->rows * d->cols * esz >= kMaxBytes) return CONV_E_UNSUPPORTED;
+  return CONV_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int64_t conv_head_loss_ws_bytes(const conv_head_desc* d, int32_t grad) {
+  const conv_status st = head_check(d);
+  // operands that need a copy only for their alignment are counted in
+  return st != CONV_OK ? (int64_t)st : head_plan(*d, grad != 0, true, true).bytes;
+}
+
+conv_status conv_head_loss(const conv_head_desc* d, const void* x, const void* w, const void* labels,
+                           const float* weights, float* loss, float* total, void* ws, int64_t ws_bytes,
+                           void* stream) {
+  return head_run(d, x, w, labels, weights, loss, total, nullptr, nullptr, ws, ws_bytes, stream, false);
+}
+
+conv_status conv_head_loss_grad(const conv_head_desc* d, const void* x, const void* w, const void* labels,
+                                const float* weights, float* loss, float* total, void* dx, void* dw, void* ws,
+                                int64_t ws_bytes, void* stream) {
+  return head_run(d, x, w, labels, weights, loss, total, dx, dw, ws, ws_bytes, stream, true);
+}
+
+int64_t conv_orthogonalize_ws_bytes(const conv_ortho_desc* d) {
+  const conv_status st = ortho_check(d);
+  return st != CONV_OK ? (int64_t)st : ortho_ws_bytes(*d);
+}
+
+conv_status conv_orthogonalize(const conv_ortho_desc* d, const void* g, void* out, void* ws, int64_t ws_bytes,
+                               void* stream) {
+  if (!d || !g || !out || !ws) return CONV_E_NULL;
+  const int64_t need = conv_orthogonalize_ws_bytes(d);
+  if (need < 0) return (conv_status)need;
+  const int64_t esz = d->dtype == CONV_F32 ? 4 : 2, count = d->batch * d->rows * d->cols;
+  if ((uintptr_t)g & (esz - 1) || (uintptr_t)out & 1 || (uintptr_t)ws & 255) return CONV_E_ALIGN;
+  if (need > ws_bytes) return CONV_E_SCRATCH;
+  const Range in[] = {{g, count * esz}};
+  const Range res[] = {{out, count * 2}, {ws, need}};
+  if (aliased(in, res)) return CONV_E_ALIAS;
+  OrthoArgs a = {};
+  a.g = g;
+  a.out = static_cast<uint16_t*>(out);
+  a.ws = static_cast<char*>(ws);
+  a.batch = (int)d->batch;
+  a.rows = (int)d->rows;
+  a.cols = (int)d->cols;
+  a.steps = d->steps;
+  a.a = d->a;
+  a.b = d->b;
+  a.c = d->c;
+  a.eps = d->eps;
+  a.g_f32 = d->dtype == CONV_F32;
+  return hip_status(launch_ortho(a, static_cast<hipStream_t>(stream)));
+}
 
 int64_t conv_group_norm_ws_bytes(const conv_norm_desc* d, int32_t grad) {
   const conv_status st = norm_check(d);

@@ -27,6 +27,17 @@ class _NormDesc(ctypes.Structure):
                 ("act", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
+class _HeadDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("c", ctypes.c_int64), ("classes", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("label_bytes", ctypes.c_int32)]
+
+
+class _OrthoDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 _bound = None
 
 
@@ -43,6 +54,17 @@ def _L():
         L.conv_group_norm.restype = ctypes.c_int
         L.conv_group_norm_grad.argtypes = [ND] + [P] * 9 + [I64, P]
         L.conv_group_norm_grad.restype = ctypes.c_int
+        HD, OD = ctypes.POINTER(_HeadDesc), ctypes.POINTER(_OrthoDesc)
+        L.conv_head_loss_ws_bytes.argtypes = [HD, I32]
+        L.conv_head_loss_ws_bytes.restype = I64
+        L.conv_head_loss.argtypes = [HD] + [P] * 7 + [I64, P]
+        L.conv_head_loss.restype = ctypes.c_int
+        L.conv_head_loss_grad.argtypes = [HD] + [P] * 9 + [I64, P]
+        L.conv_head_loss_grad.restype = ctypes.c_int
+        L.conv_orthogonalize_ws_bytes.argtypes = [OD]
+        L.conv_orthogonalize_ws_bytes.restype = I64
+        L.conv_orthogonalize.argtypes = [OD, P, P, P, I64, P]
+        L.conv_orthogonalize.restype = ctypes.c_int
         _bound = L
     return _bound
 
@@ -168,3 +190,130 @@ def group_norm_grad(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gamm
                                 _lib._stream_handle(stream))
     _lib._check(st, "conv_group_norm_grad")
     return dx, dgamma, dbeta
+
+
+# ------------------------------------------------------------------- head loss --
+
+def _head_desc(x, w, labels, weights) -> _HeadDesc:
+    if w.dim() == 4 and w.shape[1] == w.shape[2] == 1:
+        classes, c = w.shape[0], w.shape[3]  # OHWI of a 1x1 layer
+    elif w.dim() == 2:
+        classes, c = w.shape
+    else:
+        raise ValueError("w must be [classes, c] (or OHWI [classes, 1, 1, c])")
+    if x.dim() < 2 or x.shape[-1] != c:
+        raise ValueError("x must be [..., c] with w's %d channels" % c)
+    rows = x.numel() // c if c else 0
+    _dev(x, "x", torch.bfloat16, x.shape)
+    _dev(w, "w", torch.bfloat16, w.shape)
+    if labels.dtype not in (torch.int32, torch.int64):
+        raise ValueError("labels must be int32 or int64")
+    _dev(labels, "labels", labels.dtype, x.shape[:-1])
+    if weights is not None:
+        _dev(weights, "weights", torch.float32, x.shape[:-1])
+    return _HeadDesc(rows, c, classes, _lib.DTYPES["bf16"], labels.element_size())
+
+
+def head_loss_ws_bytes(rows: int, c: int, classes: int, grad: bool = False) -> int:
+    """Bytes of ``ws`` that head_loss (or head_loss_grad) takes."""
+    need = _L().conv_head_loss_ws_bytes(_HeadDesc(rows, c, classes, _lib.DTYPES["bf16"], 8), int(grad))
+    if need < 0:
+        _lib._check(int(need), "conv_head_loss_ws_bytes")
+    return int(need)
+
+
+def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weights: Optional[torch.Tensor] = None,
+              loss: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None,
+              ws: Optional[torch.Tensor] = None, stream=None):
+    """(total, loss): the softmax cross entropy of each pixel of x [..., c]
+    under the 1x1 head w [classes, c] (both bfloat16) and its weighted sum,
+    or mean when weights is None, as float32. labels [...] int32 or int64; a
+    pixel whose label lies outside 0 .. classes-1 is left out."""
+    L = _L()
+    d = _head_desc(x, w, labels, weights)
+    loss, total = _loss_outputs(x, loss, total)
+    ws = _scratch(L.conv_head_loss_ws_bytes(d, 0), ws, x.device, "conv_head_loss")
+    st = L.conv_head_loss(d, x.data_ptr(), w.data_ptr(), labels.data_ptr(), _ptr(weights), loss.data_ptr(),
+                          total.data_ptr(), *_ws_args(ws), _lib._stream_handle(stream))
+    _lib._check(st, "conv_head_loss")
+    return total, loss
+
+
+def _loss_outputs(x, loss, total):
+    if loss is None:
+        loss = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        _dev(loss, "loss", torch.float32, x.shape[:-1])
+    if total is None:
+        total = torch.empty((), dtype=torch.float32, device=x.device)
+    else:
+        _dev(total, "total", torch.float32, ())
+    return loss, total
+
+
+def head_loss_grad(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   loss: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None,
+                   dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None, stream=None):
+    """(total, loss, dx, dw): head_loss and the gradients of total, bfloat16
+    in the shapes of x and w."""
+    L = _L()
+    d = _head_desc(x, w, labels, weights)
+    loss, total = _loss_outputs(x, loss, total)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _dev(dx, "dx", x.dtype, x.shape)
+    if dw is None:
+        dw = torch.empty(w.shape, dtype=w.dtype, device=w.device)
+    else:
+        _dev(dw, "dw", w.dtype, w.shape)
+    ws = _scratch(L.conv_head_loss_ws_bytes(d, 1), ws, x.device, "conv_head_loss_grad")
+    st = L.conv_head_loss_grad(d, x.data_ptr(), w.data_ptr(), labels.data_ptr(), _ptr(weights), loss.data_ptr(),
+                               total.data_ptr(), dx.data_ptr(), dw.data_ptr(), *_ws_args(ws),
+                               _lib._stream_handle(stream))
+    _lib._check(st, "conv_head_loss_grad")
+    return total, loss, dx, dw
+
+
+# ------------------------------------------------------------ orthogonalisation --
+
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def _ortho_desc(g, steps, coeffs, eps) -> _OrthoDesc:
+    if g.dim() < 2 or g.dtype not in _FLOATS:
+        raise ValueError("g must be float32 or bfloat16, [m, n], [batch, m, n] or OHWI [c_out, kh, kw, c_in]")
+    _dev(g, "g", g.dtype, g.shape)
+    if g.dim() == 3:
+        batch, rows, cols = g.shape
+    else:
+        batch, rows = 1, g.shape[0]
+        cols = g.numel() // rows if rows else 0
+    a, b, c = coeffs
+    return _OrthoDesc(batch, rows, cols, _FLOATS[g.dtype], steps, a, b, c, eps)
+
+
+def orthogonalize_ws_bytes(batch: int, rows: int, cols: int) -> int:
+    """Bytes of ``ws`` that orthogonalize takes for [batch, rows, cols]."""
+    need = _L().conv_orthogonalize_ws_bytes(_OrthoDesc(batch, rows, cols, 0, 1, 1.0, 0.0, 0.0, 0.0))
+    if need < 0:
+        _lib._check(int(need), "conv_orthogonalize_ws_bytes")
+    return int(need)
+
+
+def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = MUON_COEFFS, eps: float = 1e-7,
+                  out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The Newton-Schulz orthogonalisation of g, bfloat16 in g's shape: g
+    [m, n], a batch [b, m, n] of matrices, or one layer's OHWI weight gradient
+    [c_out, kh, kw, c_in] as the matrix [c_out, kh kw c_in]."""
+    L = _L()
+    d = _ortho_desc(g, steps, coeffs, eps)
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    else:
+        _dev(out, "out", torch.bfloat16, g.shape)
+    ws = _scratch(L.conv_orthogonalize_ws_bytes(d), ws, g.device, "conv_orthogonalize")
+    st = L.conv_orthogonalize(d, g.data_ptr(), out.data_ptr(), *_ws_args(ws), _lib._stream_handle(stream))
+    _lib._check(st, "conv_orthogonalize")
+    return out

@@ -18,7 +18,8 @@
  * that may run at the same time need a ws each. Too small a ws is
  * CONV_E_SCRATCH. Every result is the same on every run: no atomic adds.
  * An output overlapping an input, another output or ws is CONV_E_ALIAS.
- * Each tensor and ws must be smaller than 2^31 bytes (CONV_E_UNSUPPORTED).
+ * Each tensor must be smaller than 2^31 bytes (CONV_E_UNSUPPORTED); ws may
+ * be larger.
  */
 #ifndef CONV_TRAIN_H
 #define CONV_TRAIN_H
@@ -76,6 +77,80 @@ conv_status conv_group_norm(const conv_norm_desc* d, const void* x, const float*
 conv_status conv_group_norm_grad(const conv_norm_desc* d, const void* x, const void* dy, const float* stats,
                                  const float* gamma, const float* beta, void* dx, float* dgamma, float* dbeta,
                                  void* ws, int64_t ws_bytes, void* stream);
+
+/* Softmax cross entropy of a 1x1 head: rows are the pixels (n * h * w) of a
+ * map of c channels, the head has one weight row per class.
+ *   s[r][v] = sum_k x[r][k] w[v][k]
+ *   loss[r] = log(sum_v e^s[r][v]) - s[r][labels[r]]
+ *   total   = sum_r weight[r] loss[r]
+ * A row whose label lies outside 0 .. classes-1 (-100, say) is left out:
+ * its loss is 0, its gradient row is 0, and its x is not used (whatever it
+ * holds). weights NULL takes the mean: 1 / (rows not left out), and a total
+ * of 0 when all are. The logits are never stored: the forward pass keeps one
+ * (maximum, sum of exponentials) per row and run of classes; the gradient
+ * computes them again, a piece of the classes at a time. */
+typedef struct conv_head_desc {
+  int64_t rows, c, classes;
+  int32_t dtype;       /* of x, w, dx, dw: CONV_BF16 */
+  int32_t label_bytes; /* 4 (int32) or 8 (int64) */
+} conv_head_desc;
+
+/* Scratch of conv_head_loss (grad = 0) or conv_head_loss_grad (grad = 1). */
+int64_t conv_head_loss_ws_bytes(const conv_head_desc* d, int32_t grad);
+
+/*   x       : device [rows][c] (an NHWC map)
+ *   w       : device [classes][c] (OHWI of a 1x1 layer)
+ *   labels  : device int32 or int64 [rows]
+ *   weights : device float[rows] or NULL
+ *   loss    : device float[rows]
+ *   total   : device float[1]
+ * Logits, sums and losses in fp32 from the bf16 products. Alignment: x, w to
+ * 2 bytes (16 with c % 8 == 0 is read in place, otherwise through a copy in
+ * ws), ws to 256. CONV_E_SHAPE: a size <= 0. CONV_E_UNSUPPORTED: dtype,
+ * label_bytes, c over 65536, rows or classes over 2^22 - 64, or a size
+ * limit. */
+conv_status conv_head_loss(const conv_head_desc* d, const void* x, const void* w, const void* labels,
+                           const float* weights, float* loss, float* total, void* ws, int64_t ws_bytes,
+                           void* stream);
+
+/* The same and the gradients of total:
+ *   g[r][v] = weight[r] (softmax(s[r])[v] - [v == labels[r]])
+ *   dx[r]   = sum_v g[r][v] w[v],   dw[v] = sum_r g[r][v] x[r]
+ *   dx : device [rows][c], dw : device [classes][c], bf16
+ * g is rounded to bf16 once for the two products (half a bf16 step of each
+ * term; the sums run in fp32 and are rounded to bf16 once). */
+conv_status conv_head_loss_grad(const conv_head_desc* d, const void* x, const void* w, const void* labels,
+                                const float* weights, float* loss, float* total, void* dx, void* dw, void* ws,
+                                int64_t ws_bytes, void* stream);
+
+/* Orthogonalised update of weight matrices (the update of the Muon
+ * optimiser): with X0 = G / (|G|_F + eps), m <= n after transposing a tall G,
+ *   X <- a X + (b A + c A A) X,  A = X X^T,  `steps` times,
+ * which drives every singular value of X towards 1, one matrix per batch
+ * entry. A convolution's OHWI weights are the matrix [c_out][kh kw c_in]. */
+typedef struct conv_ortho_desc {
+  int64_t batch, rows, cols;
+  int32_t dtype; /* of g: CONV_F32 or CONV_BF16; the result is CONV_BF16 */
+  int32_t steps; /* 1 .. 100 */
+  float a, b, c; /* finite */
+  float eps;     /* >= 0, finite */
+} conv_ortho_desc;
+
+int64_t conv_orthogonalize_ws_bytes(const conv_ortho_desc* d);
+
+/*   g   : device [batch][rows][cols] of dtype
+ *   out : device [batch][rows][cols] bf16 (one RNE rounding)
+ * The products run on fp16 matrix instructions with fp32 sums; X is held as a
+ * pair of fp16 (22 bits), the diagonals of A and of the polynomial in fp32,
+ * so that the result is off by less than half of a bf16 step for
+ * coefficients that keep the singular values within [0, 2]. Values are
+ * scaled by powers of two to stay in fp16's range; coefficients under which
+ * the iteration diverges give infinities or NaN, as they would in fp32. The
+ * norm is summed in 64 bits. A zero matrix with eps > 0 gives zeros.
+ * CONV_E_SHAPE: a size <= 0, steps or a coefficient out of range.
+ * CONV_E_UNSUPPORTED: dtype, batch > 65535, a side over 32768, a size limit. */
+conv_status conv_orthogonalize(const conv_ortho_desc* d, const void* g, void* out, void* ws, int64_t ws_bytes,
+                               void* stream);
 
 #ifdef __cplusplus
 }
