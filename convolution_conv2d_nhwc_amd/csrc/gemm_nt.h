@@ -163,20 +163,21 @@ gemm_nt_kernel(GemmArgs g, typename Epi::Args e) {
 
   const int kt0 = blockIdx.y * g.kt_per;
   const int nkt_all = (g.kbytes + kKB - 1) / kKB;
-  const int nkt = min(g.kt_per, nkt_all - kt0);
+  const int nkt = min(g.kt_per, nkt_all - kt0);  // <= 0: a split past the end, its sums are zeros
   const int wave_blk = wave * 1024;
   // chunk c of K-tile kt into LDS buffer buf; K past the end reads zeros
   auto dma_chunk = [&](int kt, int buf, auto cc) {
     constexpr int c = decltype(cc)::value;
     const bool in = kt * kKB + c16 < g.kbytes;
+    const int so = kt < nkt_all ? kt * kKB : 0;  // a scalar offset past the buffer could wrap its bounds check
     if constexpr (c < ACH) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           ra, (__attribute__((address_space(3))) void*)(As + buf * TQ * kKB + c * 4096 + wave_blk), 16,
-          (int)(in ? va[c] : kPastEnd), kt * kKB, 0, 0);
+          (int)(in ? va[c] : kPastEnd), so, 0, 0);
     } else {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rb, (__attribute__((address_space(3))) void*)(Bs + buf * TP * kKB + (c - ACH) * 4096 + wave_blk), 16,
-          (int)(in ? vb[c - ACH] : kPastEnd), kt * kKB, 0, 0);
+          (int)(in ? vb[c - ACH] : kPastEnd), so, 0, 0);
     }
   };
   auto dma_all = [&](int kt, int buf) {
@@ -269,9 +270,8 @@ hipError_t gemm_launch_t(GemmArgs g, const typename Epi::Args& e, int splits, in
   while (g.group < nq && 8 * g.group * g.group < nq * np) ++g.group;
   const int nkt = cdiv(g.kbytes, kKB);
   g.kt_per = cdiv(nkt, splits);
-  const int ny = cdiv(nkt, g.kt_per);
   const int tiles = Epi::kSymmetric ? np * (np + 1) / 2 : nq * np;
-  hipLaunchKernelGGL((gemm_nt_kernel<DT, T, T, Epi>), dim3(tiles, ny, batch), dim3(256), 0, s, g, e);
+  hipLaunchKernelGGL((gemm_nt_kernel<DT, T, T, Epi>), dim3(tiles, splits, batch), dim3(256), 0, s, g, e);
   return hipGetLastError();
 }
 

@@ -19,6 +19,8 @@
 // statistics and a second one that applies them; the second read of x comes
 // from the last-level cache as far as the map fits there. The gradient does the
 // same with two tensors and per-channel sums.
+#include <algorithm>
+
 #include "device_common.h"
 #include "train.h"
 
@@ -109,7 +111,8 @@ __device__ __forceinline__ float norm_slope(float z) {
     const float t = __expf(fminf(z, 20.0f));
     const float u = t * (t + 2.0f);
     const float r = __builtin_amdgcn_rcpf(u + 2.0f);
-    const float zc = fminf(fmaxf(z, -104.0f), 104.0f);  // t is 0 below, 1 - h^2 is 0 above
+    // t is 0 below, 1 - h^2 is 0 above; a NaN stays one
+    const float zc = z < -104.0f ? -104.0f : z > 104.0f ? 104.0f : z;
     return u * r + zc * (4.0f * t * (1.0f + t)) * (r * r);
   } else if constexpr (ACT == ACT_RELU) {
     return z > 0.0f ? 1.0f : 0.0f;
@@ -643,7 +646,7 @@ NormPlan norm_plan(const conv_norm_desc& d, bool grad, int align) {
   } else {
     // 128-byte runs of channels per pixel, where whole groups allow it
     const int unit = gpt0 * cg, want = 128 / esz;
-    int k = (want + unit - 1) / unit;
+    int k = std::min((want + unit - 1) / unit, (g + gpt0 - 1) / gpt0);
     while (k > 1 && k * unit > kMaxCt) --k;
     p.gpt = k * gpt0;
     p.ct = p.gpt * cg;

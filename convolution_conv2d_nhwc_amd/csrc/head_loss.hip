@@ -513,20 +513,15 @@ hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s) {
       const int64_t stride = std::min(p.vp, a.classes) * p.cq;
       const PartEpi::Args pe = {part, stride, (int)nv, (int)p.cq, 0};
       CONV_TRY((gemm_launch<BF16, PartEpi>(gw, pe, p.dw.tile, p.dw.splits, 1, s)));
-      const int ny = cdiv(cdiv(gw.kbytes, kKB), cdiv(cdiv(gw.kbytes, kKB), p.dw.splits));
-      CONV_TRY(launch_part_sum(part, stride, ny, nv, a.c, p.cq, dw, vec_dw, s));
+      CONV_TRY(launch_part_sum(part, stride, p.dw.splits, nv, a.c, p.cq, dw, vec_dw, s));
     } else {
       const StoreEpi::Args st = {dw, (int)nv, (int)a.c, vec_dw};
       CONV_TRY((gemm_launch<BF16, StoreEpi>(gw, st, p.dw.tile, 1, 1, s)));
     }
   }
-  if (p.o_dxp >= 0) {
-    // the first piece is the widest: it wrote every split that a later one adds to
-    const int nkt = cdiv(up(std::min(p.vp, a.classes), 8) * 2, kKB);
-    const int ny = cdiv(nkt, cdiv(nkt, p.dx.splits));
-    CONV_TRY(launch_part_sum(reinterpret_cast<float*>(at(p.o_dxp)), dx_stride, ny, a.rows, a.c, p.cq, a.dx, vec_dx,
-                             s));
-  }
+  if (p.o_dxp >= 0)
+    CONV_TRY(launch_part_sum(reinterpret_cast<float*>(at(p.o_dxp)), dx_stride, p.dx.splits, a.rows, a.c, p.cq, a.dx,
+                             vec_dx, s));
   return hipSuccess;
 }
 
