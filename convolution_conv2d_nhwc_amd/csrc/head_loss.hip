@@ -5,182 +5,190 @@
 // sum = sum_v e^(s - m): loss = log(sum) - (s[label] - m), and with
 // lse = m + log(sum) and the row's weight k:
 //   g[r][v] = k (e^(s - lse) - [v == label]),  dx = g w,  dw = g^T x.
+// Exponentials run in base 2 (e^s = 2^(s L), L = log2 e, one fused multiply-add
+// and one instruction a value); m and lse are kept in those units too, so that
+// the rounding of m L cancels out of every term.
 //
 // Forward: one matrix product whose epilogue keeps a (maximum, sum) pair per
-// row and half tile of classes, then one wave per row merges the pairs. A
+// row and wave's run of classes, then a reduction over the row's pairs. A
 // lane of the MFMA result holds four consecutive classes of one row, so the
-// reduction is in registers but for two exchanges between lanes.
+// epilogue's reduction is in registers but for two exchanges between lanes.
 //
 // Gradients: per piece of the classes the same product again, its epilogue
-// writing g in bf16 both row-major (for dx) and transposed (for dw; a 4x4
-// exchange within quads of lanes makes its stores vectors), then the two
-// products. Computing the logits twice costs 2 of 8 products' worth of
-// operations; the alternative, keeping e^(s - m) of each tile from the first
-// pass, rounds twice to bf16 and stores rows * classes values all the same.
-// What bounds it: the matrix cores at large sizes, launches at small ones.
-#include "gemm_nt.h"
+// writing g in bf16, then the two products, which read g, w and x as they lie
+// (see gemm.h: no transposed copies). Computing the logits twice costs 2 of 8
+// products' worth of operations; the alternative, keeping e^(s - m) of each
+// tile from the first pass, rounds twice to bf16 and stores rows * classes
+// values all the same.
+//
+// Precision. Rounding g to bf16 would cost as much as the rounding of the
+// results, nearly all of it from the one large entry of a row, its label's.
+// What that rounding left out, delta[r], is kept in fp32 and put back: in dx as
+// delta[r] w[label] in the epilogue, in dw as the product's sparse term.
+#include "gemm.h"
 #include "train.h"
 
 namespace convnhwc {
 namespace {
 
 constexpr int kMaxSplit = 16;
+constexpr float kLog2e = 1.44269504088896f;
+
+__device__ __forceinline__ float exp2_f32(float v) { return __builtin_amdgcn_exp2f(v); }
 
 __device__ __forceinline__ int label_at(const void* labels, int bytes, int64_t r, int64_t classes) {
-  const int64_t l = bytes == 8 ? static_cast<const int64_t*>(labels)[r] : static_cast<const int32_t*>(labels)[r];
+  const int64_t l = label_raw(labels, bytes, r);
   return l >= 0 && l < classes ? (int)l : -1;
 }
 
 // ---- copies ---------------------------------------------------------------------
 
-// src [rows][c] -> dst [rows][cpad] (zero past c; not when null) and
-// dst_t [c][pitch_t] (zero past rows; not when null), 64x64 tiles through
-// LDS. With labels, rows that are left out become zeros: their x, NaN or
-// not, then adds nothing to dw.
-template <int VEC>
-__global__ __launch_bounds__(256) void copy_kernel(const uint16_t* src, int64_t rows, int c, const void* labels,
-                                                   int label_bytes, int64_t classes, uint16_t* dst, int cpad,
-                                                   uint16_t* dst_t, int64_t pitch_t) {
-  __shared__ uint16_t t[64][66];
-  const int tid = threadIdx.x;
-  const int c0 = blockIdx.x * 64;
-  const int64_t r0 = (int64_t)blockIdx.y * 64;
-  constexpr int PER = 64 / VEC;  // vectors per tile row
-  for (int i = tid; i < 64 * PER; i += 256) {
-    const int r = i / PER, k = (i % PER) * VEC;
-    const int64_t row = r0 + r;
-    uint16_t v[VEC];
+// src [rows][c] -> dst [rows][cpad], zeros past c, eight values a lane. With
+// labels, rows that are left out become zeros: their x, NaN or not, then
+// adds nothing to dw.
+__device__ __forceinline__ void pad_chunk(const uint16_t* src, int64_t row, int c, int chunk, bool keep, uint16_t* dst,
+                                          int cpad) {
+  const uint16_t* p = src + row * c + chunk * 8;
+  const int left = keep ? c - chunk * 8 : 0;
+  uint16_t v[8];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = 0;
-    const bool in = row < rows && (!labels || label_at(labels, label_bytes, row, classes) >= 0);
-    if constexpr (VEC == 8) {
-      if (in && c0 + k < c) {
-        const uint4 q = *reinterpret_cast<const uint4*>(src + row * c + c0 + k);
-        __builtin_memcpy(v, &q, 16);
-      }
-      if (dst && row < rows && c0 + k < cpad) {
-        uint4 q;
-        __builtin_memcpy(&q, v, 16);
-        *reinterpret_cast<uint4*>(dst + row * cpad + c0 + k) = q;
-      }
-    } else {
-      if (in && c0 + k < c) v[0] = src[row * c + c0 + k];
-      if (dst && row < rows && c0 + k < cpad) dst[row * cpad + c0 + k] = v[0];
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) t[r][k + j] = v[j];
-  }
-  if (!dst_t) return;
-  __syncthreads();
-  for (int i = tid; i < 64 * 8; i += 256) {
-    const int k = i / 8, r = (i % 8) * 8;
-    if (c0 + k >= c || r0 + r >= pitch_t) continue;
-    uint16_t v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = t[r + j][k];
-    uint4 q;
-    __builtin_memcpy(&q, v, 16);
-    *reinterpret_cast<uint4*>(dst_t + (int64_t)(c0 + k) * pitch_t + r0 + r) = q;
+  for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : (uint16_t)0;
+  uint4 q;
+  __builtin_memcpy(&q, v, 16);
+  *reinterpret_cast<uint4*>(dst + row * cpad + chunk * 8) = q;
+}
+
+// x (nx rows, labels) and w (nw rows) in one launch; a count of 0 leaves one out.
+__global__ __launch_bounds__(256) void pad_kernel(const uint16_t* x, int64_t nx, const void* labels, int label_bytes,
+                                                  int64_t classes, uint16_t* xd, const uint16_t* w, int64_t nw,
+                                                  uint16_t* wd, int c, int cpad) {
+  const int chunks = cpad / 8;
+  const int64_t total = (nx + nw) * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / chunks;
+    const int k = (int)(i - row * chunks);
+    if (row < nx)
+      pad_chunk(x, row, c, k, label_at(labels, label_bytes, row, classes) >= 0, xd, cpad);
+    else
+      pad_chunk(w, row - nx, c, k, true, wd, cpad);
   }
 }
 
 // ---- forward ----------------------------------------------------------------------
 
 struct StatEpi {
-  static constexpr bool kSymmetric = false;
+  static constexpr bool kSymmetric = false, kSparse = false;
   struct Args {
-    float2* stat;  // [rows][slots]
+    float2* stat;  // [rows][slots]: (m L, sum 2^(s L - m L)) of the slot's classes
     float* lab;    // [rows]: the label's logit
     const void* labels;
     int label_bytes, rows, classes, slots;
   };
-  template <int TQ, int TP>
-  static __device__ __forceinline__ void run(f32x4 (&acc)[TQ / 32][TP / 32], const TileAt& at, const Args& e) {
-    constexpr int FQ = TQ / 32, FP = TP / 32;
-    const int slot = (at.tq / TQ) * 2 + at.wq;
-    const bool ragged = at.tq + TQ > e.classes;
+  template <int FQ, int FP>
+  using Pre = NoPre;
+  template <int FQ, int FP>
+  static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e, NoPre) {
+    if (at.wq + 16 * FQ > e.classes)
+      rows_of<FQ, FP, true>(acc, at, e);
+    else
+      rows_of<FQ, FP, false>(acc, at, e);
+  }
+  template <int FQ, int FP, bool RAGGED>
+  static __device__ __forceinline__ void rows_of(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e) {
+    const int slot = at.wq / (16 * FQ);
     StaticFor<0, FP>::run([&](auto jc) {
       constexpr int j = decltype(jc)::value;
+      asm volatile("" ::: "memory");  // one row at a time: keeps the registers within bounds
       const int r = at.p0 + 16 * j;
-      const int lab = r < e.rows ? label_at(e.labels, e.label_bytes, r, e.classes) : -1;
-      if (ragged) {
-#pragma unroll
-        for (int i = 0; i < FQ; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (at.q0 + 16 * i + k >= e.classes) acc[i][j][k] = -INFINITY;
-      }
+      auto val = [&](int i, int k) {
+        return RAGGED && at.q0 + 16 * i + k >= e.classes ? -INFINITY : acc[i][j][k];
+      };
       float m = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < FQ; ++i) m = fmaxf(fmaxf(m, fmaxf(acc[i][j][0], acc[i][j][1])), fmaxf(acc[i][j][2], acc[i][j][3]));
+      for (int i = 0; i < FQ; ++i) m = fmaxf(fmaxf(fmaxf(fmaxf(m, val(i, 0)), val(i, 1)), val(i, 2)), val(i, 3));
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
       // a run without a finite value has no exponentials to sum
-      const float base = m == -INFINITY ? 0.0f : m;
+      const float base = m == -INFINITY ? 0.0f : m * kLog2e;
       float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < FQ; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s += __expf(acc[i][j][k] - base);
+        for (int k = 0; k < 4; ++k) s += exp2_f32(__builtin_fmaf(val(i, k), kLog2e, -base));
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
       if (r < e.rows) {
-        if (at.lane < 16) e.stat[(int64_t)r * e.slots + slot] = float2{m, s};
-        const int d = lab - at.q0;  // this lane's classes: q0 + 16 i + 0..3
-        if (lab >= 0 && d >= 0 && d < 16 * FQ && (d & 15) < 4) {
-          float v = 0.0f;
+        if (at.lane < 16) e.stat[(int64_t)r * e.slots + slot] = float2{m == -INFINITY ? m : base, s};
+        // the label's logit, where it is one of this lane's: q0 + 16 i + 0..3
+        const int d = label_at(e.labels, e.label_bytes, r, e.classes) - at.q0;
+        if (d >= 0 && d < 16 * FQ && (d & 15) < 4) {
+          float u = 0.0f;
 #pragma unroll
           for (int i = 0; i < FQ; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (d == 16 * i + k) v = acc[i][j][k];
-          e.lab[r] = v;
+              if (d == 16 * i + k) u = acc[i][j][k];
+          e.lab[r] = u;
         }
       }
     });
   }
 };
 
-// One wave per row: the slots' pairs to lse and loss.
-__global__ __launch_bounds__(256) void rows_kernel(const float2* stat, int slots, const float* lab,
-                                                   const void* labels, int label_bytes, int64_t rows, int64_t classes,
-                                                   float* lse, float* loss) {
+struct FinishArgs {
+  const float2* stat;
+  const float* lab;
+  const void* labels;
+  const float* weights;
+  const uint16_t* x;  // to be copied to xd, rows left out as zeros; null: not
+  uint16_t* xd;
+  float* lse;   // null without gradients
+  float* loss;
+  float* inv;   // 1 / rows not left out; null without gradients
+  float* total;
+  int64_t rows, classes;
+  int slots, label_bytes, c;
+};
+
+// One row's loss and lse from its sum over the classes (in units of 2^base).
+__device__ __forceinline__ float row_loss(const FinishArgs& a, int64_t r, float base, float s, float lab, bool kept,
+                                          bool store) {
+  const float ls = __log2f(s);
+  const float loss = kept ? (ls - __builtin_fmaf(lab, kLog2e, -base)) * 0.693147180559945f : 0.0f;
+  if (store) {
+    a.loss[r] = loss;
+    // a left out row's logits are zeros in the gradient's product: 2^(0 - 0), times 0
+    if (a.lse) a.lse[r] = kept ? base + ls : 0.0f;
+  }
+  return loss;
+}
+
+// One wave per row.
+__global__ __launch_bounds__(256) void rows_kernel(FinishArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= rows) return;
-  const float2* q = stat + r * slots;
+  if (r >= a.rows) return;
+  const bool kept = label_at(a.labels, a.label_bytes, r, a.classes) >= 0;
+  if (a.x)
+    for (int k = lane; k < a.c / 8; k += 64)
+      reinterpret_cast<uint4*>(a.xd + r * a.c)[k] =
+          kept ? reinterpret_cast<const uint4*>(a.x + r * a.c)[k] : uint4{0, 0, 0, 0};
+  const float2* q = a.stat + r * a.slots;
   float m = -INFINITY;
-  for (int i = lane; i < slots; i += 64) m = fmaxf(m, q[i].x);
+  for (int i = lane; i < a.slots; i += 64) m = fmaxf(m, q[i].x);
 #pragma unroll
   for (int k = 32; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
   const float base = m == -INFINITY ? 0.0f : m;
   float s = 0.0f;
-  for (int i = lane; i < slots; i += 64) s += q[i].y * __expf(q[i].x - base);
+  for (int i = lane; i < a.slots; i += 64) s += q[i].y * exp2_f32(q[i].x - base);
 #pragma unroll
   for (int k = 32; k >= 1; k >>= 1) s += __shfl_xor(s, k);
-  if (lane == 0) {
-    const float ls = logf(s);
-    const bool kept = label_at(labels, label_bytes, r, classes) >= 0;
-    if (lse) lse[r] = base + ls;
-    loss[r] = kept ? ls - (lab[r] - base) : 0.0f;
-  }
+  row_loss(a, r, base, s, kept ? a.lab[r] : 0.0f, kept, lane == 0);
 }
 
-// One workgroup: the count of rows that are not left out, every row's weight
-// and the weighted total (64-bit partial sums, a fixed order).
-__global__ __launch_bounds__(1024) void total_kernel(const void* labels, int label_bytes, int64_t rows,
-                                                     int64_t classes, const float* weights, const float* loss,
-                                                     float* scale, float* total) {
-  __shared__ double sum[16];
-  __shared__ int cnt[16];
+// The weighted total and the count from the lanes' sums (64-bit, a fixed order).
+__device__ __forceinline__ void total_store(const FinishArgs& a, double t, int n, double* sum, int* cnt) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int n = 0;
-  double t = 0.0;
-  for (int64_t r = tid; r < rows; r += 1024) {
-    const bool kept = label_at(labels, label_bytes, r, classes) >= 0;
-    n += kept;
-    if (kept) t += (double)loss[r] * (weights ? (double)weights[r] : 1.0);
-  }
 #pragma unroll
   for (int k = 32; k >= 1; k >>= 1) {
     n += __shfl_xor(n, k);
@@ -191,95 +199,223 @@ __global__ __launch_bounds__(1024) void total_kernel(const void* labels, int lab
     cnt[wave] = n;
   }
   __syncthreads();
-  n = 0;
-  t = 0.0;
-  for (int i = 0; i < 16; ++i) {
-    n += cnt[i];
-    t += sum[i];
+  if (tid == 0) {
+    n = 0;
+    t = 0.0;
+    for (int i = 0; i < 16; ++i) {
+      n += cnt[i];
+      t += sum[i];
+    }
+    const double inv = 1.0 / (double)max(n, 1);
+    a.total[0] = (float)(a.weights ? t : t * inv);
+    if (a.inv) a.inv[0] = (float)inv;
   }
-  const double inv = 1.0 / (double)max(n, 1);
-  if (tid == 0) total[0] = (float)(weights ? t : t * inv);
-  if (scale) {
-    for (int64_t r = tid; r < rows; r += 1024) {
-      const bool kept = label_at(labels, label_bytes, r, classes) >= 0;
-      scale[r] = kept ? (weights ? weights[r] : (float)inv) : 0.0f;
+}
+
+__global__ __launch_bounds__(1024) void total_kernel(FinishArgs a) {
+  __shared__ double sum[16];
+  __shared__ int cnt[16];
+  int n = 0;
+  double t = 0.0;
+#pragma unroll 4
+  for (int64_t r = threadIdx.x; r < a.rows; r += 1024) {
+    const bool kept = label_at(a.labels, a.label_bytes, r, a.classes) >= 0;
+    const double l = a.loss[r], w = a.weights ? a.weights[r] : 1.0f;
+    n += kept;
+    t += kept ? l * w : 0.0;
+  }
+  total_store(a, t, n, sum, cnt);
+}
+
+// Few rows with few pairs: everything in one launch, the rows in the first
+// workgroup (eight lanes each, up to four rows, all loads before the first
+// use: one latency), the copy of x in the others.
+constexpr int kFinishRows = 512, kFinishSlots = 64;
+
+__global__ __launch_bounds__(1024) void finish_kernel(FinishArgs a) {
+  const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {
+    const int chunks = a.c / 8;
+    const int i = (blockIdx.x - 1) * 1024 + tid;
+    if (i < (int)a.rows * chunks)
+      reinterpret_cast<uint4*>(a.xd)[i] = label_at(a.labels, a.label_bytes, i / chunks, a.classes) >= 0
+                                              ? reinterpret_cast<const uint4*>(a.x)[i]
+                                              : uint4{0, 0, 0, 0};
+    return;
+  }
+  __shared__ double sum[16];
+  __shared__ int cnt[16];
+  constexpr int N = kFinishRows / 128, S = kFinishSlots / 8;
+  const int rows = (int)a.rows, sub = tid & 7;
+  int label[N];
+  float w[N], lab[N];
+  float2 q[N][S];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int r = (tid >> 3) + 128 * u;
+    label[u] = r < rows ? label_at(a.labels, a.label_bytes, r, a.classes) : -1;
+    w[u] = r < rows && a.weights ? a.weights[r] : 1.0f;
+    lab[u] = r < rows ? a.lab[r] : 0.0f;  // of a row left out: not set, not used
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      q[u][i] = r < rows && sub + 8 * i < a.slots ? a.stat[(int64_t)r * a.slots + sub + 8 * i] : float2{-INFINITY, 0.0f};
+  }
+  int n = 0;
+  double t = 0.0;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int r = (tid >> 3) + 128 * u;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < S; ++i) m = fmaxf(m, q[u][i].x);
+#pragma unroll
+    for (int k = 4; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
+    const float base = m == -INFINITY ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) s += q[u][i].y * exp2_f32(q[u][i].x - base);
+#pragma unroll
+    for (int k = 4; k >= 1; k >>= 1) s += __shfl_xor(s, k);
+    const bool kept = label[u] >= 0;
+    const float loss = row_loss(a, r, base, s, lab[u], kept, sub == 0 && r < rows);
+    if (sub == 0 && kept) {
+      ++n;
+      t += (double)loss * w[u];
     }
   }
+  total_store(a, t, n, sum, cnt);
 }
 
 // ---- gradients -----------------------------------------------------------------
 
 struct GradEpi {
-  static constexpr bool kSymmetric = false;
+  static constexpr bool kSymmetric = false, kSparse = false;
   struct Args {
     const float* lse;
-    const float* scale;
+    const float* weights;
+    const float* inv;
     const void* labels;
     int label_bytes;
     int rows, classes;   // of the whole problem
     int v0, nv;          // the piece: classes v0 .. v0 + nv - 1
     uint16_t* ds;        // [rows][vp]
-    uint16_t* dst;       // [vp][rpad]
-    int64_t vp, rpad;
+    float* delta;        // [rows]
+    int64_t vp;
   };
-  template <int TQ, int TP>
-  static __device__ __forceinline__ void run(f32x4 (&acc)[TQ / 32][TP / 32], const TileAt& at, const Args& e) {
-    constexpr int FQ = TQ / 32, FP = TP / 32;
-    const bool ragged = at.tq + TQ > e.nv;
+  template <int FQ, int FP>
+  using Pre = NoPre;
+  template <int FQ, int FP>
+  static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e, NoPre) {
+    const bool ragged = at.wq + 16 * FQ > e.nv;
+    const float inv = e.weights ? 0.0f : e.inv[0];
     StaticFor<0, FP>::run([&](auto jc) {
       constexpr int j = decltype(jc)::value;
       const int r = at.p0 + 16 * j;
+      // rows past the last and rows left out: logits 0, lse 0, weight 0
       float lse = 0.0f, k = 0.0f;
-      int d = -1;
+      int d = -1;  // the label, from the wave's first class
       if (r < e.rows) {
-        k = e.scale[r];
-        lse = e.lse[r];
         const int lab = label_at(e.labels, e.label_bytes, r, e.classes);
-        d = lab >= 0 ? lab - e.v0 - at.q0 : -1;
-      }
-      StaticFor<0, FQ>::run([&](auto ic) {
-        constexpr int i = decltype(ic)::value;
-        float g[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          g[z] = __expf(acc[i][j][z] - lse);
-          if (d == 16 * i + z) g[z] -= 1.0f;
-          g[z] *= k;
-          // rows past the last, rows left out and classes past the last: zeros
-          if (k == 0.0f || (ragged && at.q0 + 16 * i + z >= e.nv)) g[z] = 0.0f;
+        lse = e.lse[r];
+        if (lab >= 0) {
+          k = e.weights ? e.weights[r] : inv;
+          d = lab - e.v0 - at.wq;
         }
-        const uint2 v = {bf16x2_bits(g[0], g[1]), bf16x2_bits(g[2], g[3])};
-        const int q = at.q0 + 16 * i;
-        if (r < e.rows) *reinterpret_cast<uint2*>(e.ds + (int64_t)r * e.vp + q) = v;
-        const uint2 t = quad_transpose(v, at.lane);
-        if ((r & ~3) < e.rpad)
-          *reinterpret_cast<uint2*>(e.dst + (int64_t)(q + (at.lane & 3)) * e.rpad + (r & ~3)) = t;
-      });
+      }
+      uint16_t* const row = e.ds + (int64_t)r * e.vp + at.q0;
+      if (ragged || __any(d >= 0 && d < 16 * FQ)) {
+        d -= at.q0 - at.wq;
+        StaticFor<0, FQ>::run([&](auto ic) {
+          constexpr int i = decltype(ic)::value;
+          float g[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const bool hit = d == 16 * i + z;
+            g[z] = exp2_f32(__builtin_fmaf(acc[i][j][z], kLog2e, -lse));
+            if (hit) g[z] -= 1.0f;
+            g[z] *= k;
+            if (at.q0 + 16 * i + z >= e.nv) g[z] = 0.0f;
+            if (hit) e.delta[r] = g[z] - bf16_bits_to_f32(f32_to_bf16_bits(g[z]));
+          }
+          const uint2 v = {bf16x2_bits(g[0], g[1]), bf16x2_bits(g[2], g[3])};
+          if (r < e.rows) *reinterpret_cast<uint2*>(row + 16 * i) = v;
+        });
+      } else {
+        StaticFor<0, FQ>::run([&](auto ic) {
+          constexpr int i = decltype(ic)::value;
+          float g[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) g[z] = k * exp2_f32(__builtin_fmaf(acc[i][j][z], kLog2e, -lse));
+          const uint2 v = {bf16x2_bits(g[0], g[1]), bf16x2_bits(g[2], g[3])};
+          if (r < e.rows) *reinterpret_cast<uint2*>(row + 16 * i) = v;
+        });
+      }
     });
   }
 };
 
-// bf16 out [p][q] (pitch c).
+// The label's part of dx that bf16 g left out, for the rows whose label is one
+// of the piece's classes.
+struct LabelTerm {
+  const uint16_t* w;    // [classes][cpad]
+  const void* labels;
+  const float* delta;
+  int label_bytes, classes, cpad;
+  int v0, nv;
+};
+
+struct LabelRow {
+  const uint16_t* w;
+  float delta;
+};
+__device__ __forceinline__ LabelRow label_row(const LabelTerm& t, int r) {
+  const int lab = label_at(t.labels, t.label_bytes, r, t.classes);
+  const bool in = lab >= t.v0 && lab < t.v0 + t.nv;
+  return {in ? t.w + (int64_t)lab * t.cpad : t.w, in ? t.delta[r] : 0.0f};
+}
+__device__ __forceinline__ f32x4 label_add(f32x4 v, const LabelRow& l, int q) {
+  if (l.delta != 0.0f) {
+    const uint2 u = *reinterpret_cast<const uint2*>(l.w + q);
+    v[0] += l.delta * bf16_bits_to_f32(u.x & 0xffffu);
+    v[1] += l.delta * bf16_bits_to_f32(u.x >> 16);
+    v[2] += l.delta * bf16_bits_to_f32(u.y & 0xffffu);
+    v[3] += l.delta * bf16_bits_to_f32(u.y >> 16);
+  }
+  return v;
+}
+
+// bf16 out [p][q] (pitch c). DX: with the label's term; else the product has a
+// sparse term.
+template <bool DX>
 struct StoreEpi {
-  static constexpr bool kSymmetric = false;
+  static constexpr bool kSymmetric = false, kSparse = !DX;
   struct Args {
     uint16_t* out;
     int rows, c;
     int vec;  // c % 4 == 0 and out 8-byte aligned
+    LabelTerm lt;
+    SparseTerm st;
   };
-  template <int TQ, int TP>
-  static __device__ __forceinline__ void run(f32x4 (&acc)[TQ / 32][TP / 32], const TileAt& at, const Args& e) {
-    StaticFor<0, TP / 32>::run([&](auto jc) {
+  static __device__ __forceinline__ SparseTerm sparse(const Args& e) { return e.st; }
+  template <int FQ, int FP>
+  using Pre = NoPre;
+  template <int FQ, int FP>
+  static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e, NoPre) {
+    StaticFor<0, FP>::run([&](auto jc) {
       constexpr int j = decltype(jc)::value;
       const int r = at.p0 + 16 * j;
       if (r >= e.rows) return;
-      StaticFor<0, TQ / 32>::run([&](auto ic) {
+      LabelRow l = {};
+      if constexpr (DX) l = label_row(e.lt, r);
+      StaticFor<0, FQ>::run([&](auto ic) {
         constexpr int i = decltype(ic)::value;
         const int q = at.q0 + 16 * i;
+        if (q >= e.c) return;
         uint16_t* o = e.out + (int64_t)r * e.c + q;
-        const f32x4 v = acc[i][j];
+        f32x4 v = acc[i][j];
+        if constexpr (DX) v = label_add(v, l, q);
         if (e.vec) {
-          if (q < e.c) *reinterpret_cast<uint2*>(o) = uint2{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
+          *reinterpret_cast<uint2*>(o) = uint2{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
         } else {
 #pragma unroll
           for (int z = 0; z < 4; ++z)
@@ -291,27 +427,38 @@ struct StoreEpi {
 };
 
 // fp32 partial sums [split][p][cq], added to what an earlier piece left.
+template <bool DX>
 struct PartEpi {
-  static constexpr bool kSymmetric = false;
+  static constexpr bool kSymmetric = false, kSparse = !DX;
   struct Args {
     float* part;
     int64_t split_stride;
     int rows, cq;
     int add;
+    LabelTerm lt;
+    SparseTerm st;
   };
-  template <int TQ, int TP>
-  static __device__ __forceinline__ void run(f32x4 (&acc)[TQ / 32][TP / 32], const TileAt& at, const Args& e) {
+  static __device__ __forceinline__ SparseTerm sparse(const Args& e) { return e.st; }
+  template <int FQ, int FP>
+  using Pre = NoPre;
+  template <int FQ, int FP>
+  static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e, NoPre) {
     float* base = e.part + at.split * e.split_stride;
-    StaticFor<0, TP / 32>::run([&](auto jc) {
+    StaticFor<0, FP>::run([&](auto jc) {
       constexpr int j = decltype(jc)::value;
       const int r = at.p0 + 16 * j;
       if (r >= e.rows) return;
-      StaticFor<0, TQ / 32>::run([&](auto ic) {
+      LabelRow l = {};
+      if constexpr (DX)
+        if (at.split == 0) l = label_row(e.lt, r);
+      StaticFor<0, FQ>::run([&](auto ic) {
         constexpr int i = decltype(ic)::value;
         const int q = at.q0 + 16 * i;
         if (q >= e.cq) return;
         f32x4* o = reinterpret_cast<f32x4*>(base + (int64_t)r * e.cq + q);
-        *o = e.add ? *o + acc[i][j] : acc[i][j];
+        f32x4 v = acc[i][j];
+        if constexpr (DX) v = label_add(v, l, q);
+        *o = e.add ? *o + v : v;
       });
     });
   }
@@ -349,7 +496,8 @@ GemmShape shape_for(int64_t q, int64_t p, int64_t k) {
   auto tiles = [&](int t) { return (int64_t)cdiv(q, t) * cdiv(p, t); };
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplit, k / 512));
   if (tiles(256) >= 192) return {256, 1};
-  if (tiles(128) * most >= 128) return {128, (int)std::min<int64_t>(most, cdiv(512, tiles(128)))};
+  if (tiles(256) * most >= 192) return {256, (int)std::min<int64_t>(most, cdiv(512, tiles(256)))};
+  if (tiles(128) * most >= 128) return {128, (int)std::min<int64_t>(most, cdiv(256, tiles(128)))};
   return {64, (int)std::min<int64_t>(most, cdiv(512, tiles(64)))};
 }
 
@@ -361,11 +509,10 @@ HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w)
   HeadPlan p = {};
   const int64_t rows = d.rows, c = d.c, v = d.classes;
   p.cpad = up(c, 8);
-  p.rpad = up(rows, 64);
-  p.vpad = up(v, 64);
   p.cq = up(c, 4);
   p.stat_tile = gemm_tile(v, rows, 1, false);
-  p.slots = 2 * cdiv(v, p.stat_tile);
+  p.slots = p.stat_tile == 64 ? cdiv(v, 64) : 2 * cdiv(v, p.stat_tile);  // one per wave along the classes
+  p.copy_x = copy_x;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -374,24 +521,23 @@ HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w)
   };
   p.o_stat = take(rows * p.slots * 8);
   p.o_lab = take(rows * 4);
-  p.o_lse = p.o_scale = p.o_x = p.o_w = p.o_xt = p.o_wt = p.o_ds = p.o_dst = p.o_dxp = p.o_dwp = -1;
+  p.o_lse = p.o_inv = p.o_delta = p.o_x = p.o_w = p.o_ds = p.o_dxp = p.o_dwp = -1;
   // the gradient reads x with the rows left out as zeros: always a copy
   if (grad || copy_x) p.o_x = take(rows * p.cpad * 2);
   if (copy_w) p.o_w = take(v * p.cpad * 2);
   if (grad) {
     p.o_lse = take(rows * 4);
-    p.o_scale = take(rows * 4);
-    p.o_xt = take(c * p.rpad * 2);
-    p.o_wt = take(c * p.vpad * 2);
-    // pieces of at most 512 MiB of g (and as much transposed)
-    p.vp = std::min(up(v, 256), std::max<int64_t>(256, ((int64_t)1 << 28) / p.rpad / 256 * 256));
+    p.o_delta = take(rows * 4);
+    p.o_inv = take(4);
+    // equal pieces of at most 512 MiB of g (or 256 classes)
+    const int64_t most = std::max<int64_t>(256, ((int64_t)1 << 28) / rows / 256 * 256);
+    p.vp = up(cdiv(v, cdiv(v, most)), 256);
     const bool pieces = p.vp < v;
     const int64_t pv = std::min(p.vp, v);
     p.ds_tile = gemm_tile(pv, rows, 1, false);
     p.dx = shape_for(c, rows, pv);
     p.dw = shape_for(c, pv, rows);
     p.o_ds = take(rows * p.vp * 2);
-    p.o_dst = take(p.vp * p.rpad * 2);
     if (pieces || p.dx.splits > 1) p.o_dxp = take(p.dx.splits * rows * p.cq * 4);
     if (p.dw.splits > 1) p.o_dwp = take(p.dw.splits * pv * p.cq * 4);
   }
@@ -400,21 +546,6 @@ HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w)
 }
 
 namespace {
-
-hipError_t launch_copy(const uint16_t* src, int64_t rows, int64_t c, const HeadArgs* mask, uint16_t* dst,
-                       int64_t cpad, uint16_t* dst_t, int64_t pitch_t, hipStream_t s) {
-  const dim3 grid(cdiv(cpad, 64), cdiv(dst_t ? pitch_t : rows, 64));
-  const void* labels = mask ? mask->labels : nullptr;
-  const int lb = mask ? mask->label_bytes : 4;
-  const int64_t cls = mask ? mask->classes : 0;
-  if (c % 8 == 0 && ((uintptr_t)src & 15) == 0)
-    hipLaunchKernelGGL(copy_kernel<8>, grid, dim3(256), 0, s, src, rows, (int)c, labels, lb, cls, dst, (int)cpad,
-                       dst_t, pitch_t);
-  else
-    hipLaunchKernelGGL(copy_kernel<1>, grid, dim3(256), 0, s, src, rows, (int)c, labels, lb, cls, dst, (int)cpad,
-                       dst_t, pitch_t);
-  return hipGetLastError();
-}
 
 hipError_t launch_part_sum(const float* part, int64_t stride, int splits, int64_t rows, int64_t c, int64_t cq,
                            uint16_t* out, int vec, hipStream_t s) {
@@ -435,43 +566,62 @@ hipError_t launch_part_sum(const float* part, int64_t stride, int splits, int64_
 hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s) {
   const HeadPlan& p = a.p;
   auto at = [&](int64_t o) { return a.ws + o; };
+  auto f32_at = [&](int64_t o) { return o < 0 ? nullptr : reinterpret_cast<float*>(a.ws + o); };
   const uint16_t* x = a.x;
   const uint16_t* w = a.w;
-  uint16_t* xt = grad ? reinterpret_cast<uint16_t*>(at(p.o_xt)) : nullptr;
-  uint16_t* wt = grad ? reinterpret_cast<uint16_t*>(at(p.o_wt)) : nullptr;
-  if (p.o_x >= 0) {
-    uint16_t* xc = reinterpret_cast<uint16_t*>(at(p.o_x));
-    CONV_TRY(launch_copy(a.x, a.rows, a.c, grad ? &a : nullptr, xc, p.cpad, xt, p.rpad, s));
-    x = xc;
-  }
-  if (p.o_w >= 0 || grad) {
+  uint16_t* xc = p.o_x >= 0 ? reinterpret_cast<uint16_t*>(at(p.o_x)) : nullptr;
+  if (p.copy_x || p.o_w >= 0) {
     uint16_t* wc = p.o_w >= 0 ? reinterpret_cast<uint16_t*>(at(p.o_w)) : nullptr;
-    CONV_TRY(launch_copy(a.w, a.classes, a.c, nullptr, wc, p.cpad, wt, p.vpad, s));
+    const int64_t nx = p.copy_x ? a.rows : 0, nw = wc ? a.classes : 0;
+    const int blocks = (int)std::min<int64_t>(((nx + nw) * (p.cpad / 8) + 255) / 256, 65536);
+    hipLaunchKernelGGL(pad_kernel, dim3(blocks), dim3(256), 0, s, a.x, nx, a.labels, a.label_bytes, a.classes, xc, a.w,
+                       nw, wc, (int)a.c, (int)p.cpad);
+    CONV_TRY(hipGetLastError());
+    if (p.copy_x) x = xc;
     if (wc) w = wc;
   }
   // x and w read in place have c % 8 == 0, so cpad is their pitch too
   GemmArgs g = {};
   g.a = reinterpret_cast<const char*>(w);
   g.b = reinterpret_cast<const char*>(x);
-  g.a_pitch = g.b_pitch = g.kbytes = (int)p.cpad * 2;
+  g.a_pitch = g.b_pitch = (int)p.cpad * 2;
+  g.k = (int)p.cpad;
   g.q = (int)a.classes;
   g.p = (int)a.rows;
-  float* lab = reinterpret_cast<float*>(at(p.o_lab));
-  float2* stat = reinterpret_cast<float2*>(at(p.o_stat));
-  float* lse = grad ? reinterpret_cast<float*>(at(p.o_lse)) : nullptr;
-  float* scale = grad ? reinterpret_cast<float*>(at(p.o_scale)) : nullptr;
-  const StatEpi::Args se = {stat, lab, a.labels, a.label_bytes, (int)a.rows, (int)a.classes, p.slots};
-  CONV_TRY((gemm_launch<BF16, StatEpi>(g, se, p.stat_tile, 1, 1, s)));
-  hipLaunchKernelGGL(rows_kernel, dim3(cdiv(a.rows, 4)), dim3(256), 0, s, stat, p.slots, lab, a.labels, a.label_bytes,
-                     a.rows, a.classes, lse, a.loss);
-  CONV_TRY(hipGetLastError());
-  hipLaunchKernelGGL(total_kernel, dim3(1), dim3(1024), 0, s, a.labels, a.label_bytes, a.rows, a.classes, a.weights,
-                     a.loss, scale, a.total);
+  FinishArgs f = {};
+  f.stat = reinterpret_cast<const float2*>(at(p.o_stat));
+  f.lab = f32_at(p.o_lab);
+  f.labels = a.labels;
+  f.weights = a.weights;
+  if (grad && !p.copy_x) {
+    f.x = a.x;
+    f.xd = xc;
+  }
+  f.lse = f32_at(p.o_lse);
+  f.loss = a.loss;
+  f.inv = f32_at(p.o_inv);
+  f.total = a.total;
+  f.rows = a.rows;
+  f.classes = a.classes;
+  f.slots = p.slots;
+  f.label_bytes = a.label_bytes;
+  f.c = (int)a.c;
+  const StatEpi::Args se = {reinterpret_cast<float2*>(at(p.o_stat)), f32_at(p.o_lab), a.labels, a.label_bytes,
+                            (int)a.rows, (int)a.classes, p.slots};
+  CONV_TRY((gemm_launch<BF16, false, false, StatEpi>(g, se, p.stat_tile, 1, 1, s)));
+  if (a.rows <= kFinishRows && p.slots <= kFinishSlots) {
+    const int copies = f.x ? cdiv(a.rows * (a.c / 8), 1024) : 0;
+    hipLaunchKernelGGL(finish_kernel, dim3(1 + copies), dim3(1024), 0, s, f);
+  } else {
+    hipLaunchKernelGGL(rows_kernel, dim3(cdiv(a.rows, 4)), dim3(256), 0, s, f);
+    CONV_TRY(hipGetLastError());
+    hipLaunchKernelGGL(total_kernel, dim3(1), dim3(1024), 0, s, f);
+  }
   CONV_TRY(hipGetLastError());
   if (!grad) return hipSuccess;
 
   uint16_t* ds = reinterpret_cast<uint16_t*>(at(p.o_ds));
-  uint16_t* dst = reinterpret_cast<uint16_t*>(at(p.o_dst));
+  float* delta = f32_at(p.o_delta);
   const int vec_dx = a.c % 4 == 0 && ((uintptr_t)a.dx & 7) == 0;
   const int vec_dw = a.c % 4 == 0 && ((uintptr_t)a.dw & 7) == 0;
   const int64_t dx_stride = a.rows * p.cq;
@@ -479,49 +629,52 @@ hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s) {
     const int64_t nv = std::min(p.vp, a.classes - v0);
     GemmArgs gg = g;
     gg.a = reinterpret_cast<const char*>(w + v0 * p.cpad);
+    gg.b = reinterpret_cast<const char*>(xc);
     gg.q = (int)nv;
-    const GradEpi::Args ge = {lse, scale, a.labels, a.label_bytes, (int)a.rows, (int)a.classes, (int)v0, (int)nv, ds,
-                              dst, p.vp, p.rpad};
-    CONV_TRY((gemm_launch<BF16, GradEpi>(gg, ge, p.ds_tile, 1, 1, s)));
-    // dx [rows][c] (+)= ds . (wt piece)^T
+    const GradEpi::Args ge = {f.lse, a.weights, f.inv, a.labels, a.label_bytes, (int)a.rows, (int)a.classes, (int)v0,
+                              (int)nv, ds, delta, p.vp};
+    CONV_TRY((gemm_launch<BF16, false, false, GradEpi>(gg, ge, p.ds_tile, 1, 1, s)));
+    const LabelTerm lt = {w, a.labels, delta, a.label_bytes, (int)a.classes, (int)p.cpad, (int)v0, (int)nv};
+    const SparseTerm st = {a.labels, a.label_bytes, (int)v0, delta};
+    // dx [rows][c] (+)= g . w of the piece
     GemmArgs gx = {};
-    gx.a = reinterpret_cast<const char*>(wt + v0);
+    gx.a = gg.a;
     gx.b = reinterpret_cast<const char*>(ds);
-    gx.a_pitch = (int)p.vpad * 2;
+    gx.a_pitch = (int)p.cpad * 2;
     gx.b_pitch = (int)p.vp * 2;
-    gx.kbytes = (int)up(nv, 8) * 2;
-    gx.q = (int)a.c;
+    gx.k = (int)nv;
+    gx.q = (int)p.cpad;
     gx.p = (int)a.rows;
     if (p.o_dxp >= 0) {
-      const PartEpi::Args pe = {reinterpret_cast<float*>(at(p.o_dxp)), dx_stride, (int)a.rows, (int)p.cq, v0 > 0};
-      CONV_TRY((gemm_launch<BF16, PartEpi>(gx, pe, p.dx.tile, p.dx.splits, 1, s)));
+      const PartEpi<true>::Args pe = {f32_at(p.o_dxp), dx_stride, (int)a.rows, (int)p.cq, v0 > 0, lt, st};
+      CONV_TRY((gemm_launch<BF16, true, false, PartEpi<true>>(gx, pe, p.dx.tile, p.dx.splits, 1, s)));
     } else {
-      const StoreEpi::Args st = {a.dx, (int)a.rows, (int)a.c, vec_dx};
-      CONV_TRY((gemm_launch<BF16, StoreEpi>(gx, st, p.dx.tile, 1, 1, s)));
+      const StoreEpi<true>::Args ee = {a.dx, (int)a.rows, (int)a.c, vec_dx, lt, st};
+      CONV_TRY((gemm_launch<BF16, true, false, StoreEpi<true>>(gx, ee, p.dx.tile, 1, 1, s)));
     }
-    // dw piece [nv][c] = dst . xt^T
+    // dw of the piece [nv][c] = g^T x
     GemmArgs gw = {};
-    gw.a = reinterpret_cast<const char*>(xt);
-    gw.b = reinterpret_cast<const char*>(dst);
-    gw.a_pitch = gw.b_pitch = (int)p.rpad * 2;
-    gw.kbytes = (int)up(a.rows, 8) * 2;
-    gw.q = (int)a.c;
-    gw.p = (int)nv;
+    gw.a = reinterpret_cast<const char*>(xc);
+    gw.b = reinterpret_cast<const char*>(ds);
+    gw.a_pitch = (int)p.cpad * 2;
+    gw.b_pitch = (int)p.vp * 2;
+    gw.k = (int)a.rows;
+    gw.q = (int)p.cpad;
+    gw.p = (int)up(nv, 8);
     uint16_t* dw = a.dw + v0 * a.c;
     if (p.o_dwp >= 0) {
-      float* part = reinterpret_cast<float*>(at(p.o_dwp));
+      float* part = f32_at(p.o_dwp);
       const int64_t stride = std::min(p.vp, a.classes) * p.cq;
-      const PartEpi::Args pe = {part, stride, (int)nv, (int)p.cq, 0};
-      CONV_TRY((gemm_launch<BF16, PartEpi>(gw, pe, p.dw.tile, p.dw.splits, 1, s)));
+      const PartEpi<false>::Args pe = {part, stride, (int)nv, (int)p.cq, 0, lt, st};
+      CONV_TRY((gemm_launch<BF16, true, true, PartEpi<false>>(gw, pe, p.dw.tile, p.dw.splits, 1, s)));
       CONV_TRY(launch_part_sum(part, stride, p.dw.splits, nv, a.c, p.cq, dw, vec_dw, s));
     } else {
-      const StoreEpi::Args st = {dw, (int)nv, (int)a.c, vec_dw};
-      CONV_TRY((gemm_launch<BF16, StoreEpi>(gw, st, p.dw.tile, 1, 1, s)));
+      const StoreEpi<false>::Args ee = {dw, (int)nv, (int)a.c, vec_dw, lt, st};
+      CONV_TRY((gemm_launch<BF16, true, true, StoreEpi<false>>(gw, ee, p.dw.tile, 1, 1, s)));
     }
   }
   if (p.o_dxp >= 0)
-    CONV_TRY(launch_part_sum(reinterpret_cast<float*>(at(p.o_dxp)), dx_stride, p.dx.splits, a.rows, a.c, p.cq, a.dx,
-                             vec_dx, s));
+    CONV_TRY(launch_part_sum(f32_at(p.o_dxp), dx_stride, p.dx.splits, a.rows, a.c, p.cq, a.dx, vec_dx, s));
   return hipSuccess;
 }
 

@@ -63,15 +63,14 @@ struct GemmShape {
 // Tiles, pieces and the layout of ws (byte offsets; -1: not used).
 struct HeadPlan {
   int64_t cpad;    // channels of the copies, a multiple of 8
-  int64_t rpad;    // row pitch of the transposed copies, a multiple of 64
-  int64_t vpad;    // class pitch of the transposed weights, a multiple of 64
   int64_t cq;      // pitch of the fp32 partial sums, a multiple of 4
   int64_t vp;      // classes per piece of the gradient, a multiple of 256
   int slots;       // (max, sum) pairs per row
   int stat_tile, ds_tile;
+  bool copy_x;
   GemmShape dx, dw;
-  int64_t o_stat, o_lab, o_lse, o_scale;                       // forward
-  int64_t o_x, o_w, o_xt, o_wt, o_ds, o_dst, o_dxp, o_dwp;     // copies and gradient
+  int64_t o_stat, o_lab, o_x, o_w;                       // forward, copies
+  int64_t o_lse, o_inv, o_delta, o_ds, o_dxp, o_dwp;     // gradient
   int64_t bytes;
 };
 
