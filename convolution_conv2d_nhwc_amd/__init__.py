@@ -18,5 +18,5 @@ def __getattr__(name):
         return getattr(_lib, name)
     if name in ("group_norm", "group_norm_grad", "head_loss", "head_loss_grad", "orthogonalize"):
         from . import train
-        return getattr(train, name)
+        return globals().setdefault(name, getattr(train, name))
     raise AttributeError(name)

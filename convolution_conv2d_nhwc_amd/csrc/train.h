@@ -16,7 +16,7 @@ bool ranges_overlap(const void* a, int64_t an, const void* b, int64_t bn);
 // ---- group norm ---------------------------------------------------------------
 
 // How a (n, h*w, c) map is cut: channel tiles of whole groups (tpg == 1) or
-// parts of one group (gpt == 1, tpg > 1), pixel chunks of ppi * r pixels.
+// parts of one group (gpt == 1, tpg > 1), and pixel chunks.
 struct NormPlan {
   int vec;     // elements per load
   int ct;      // channels per tile (a multiple of vec)
@@ -24,8 +24,10 @@ struct NormPlan {
   int tpg;     // tiles per group
   int ctiles;  // channel tiles
   int ppi;     // pixels a workgroup covers per step
-  int r;       // steps kept in registers
-  int chunks;  // pixel chunks per image (1 with tpg == 1: one launch)
+  int r;       // one launch: vectors a lane keeps in registers; 0: streamed
+  int threads; // lanes of a workgroup
+  int chunks;  // pixel chunks per image (one launch: 1)
+  int cpix;    // pixels per chunk, whole blocks
 };
 
 struct NormArgs {
@@ -36,8 +38,6 @@ struct NormArgs {
   void* y;       // y, or dx of the gradient
   float* stats;  // [n][groups][2]: written by the forward pass when not null, read by the gradient
   float* part;   // ws: forward [n][groups][chunks * tpg][2]; gradient [n][chunks][c][2]
-  float* tot;    // ws: gradient [n][c][2] per-image channel sums
-  float* means;  // ws: gradient [n][groups][2]
   float* dgamma;
   float* dbeta;
   int64_t pitch;  // elements per pixel of x

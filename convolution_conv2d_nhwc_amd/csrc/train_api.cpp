@@ -205,11 +205,14 @@ int64_t conv_group_norm_ws_bytes(const conv_norm_desc* d, int32_t grad) {
 conv_status conv_group_norm(const conv_norm_desc* d, const void* x, const float* gamma, const float* beta, void* y,
                             float* stats, void* ws, int64_t ws_bytes, void* stream) {
   if (!d || !x || !y) return CONV_E_NULL;
-  const int64_t need = conv_group_norm_ws_bytes(d, 0);
-  if (need < 0) return (conv_status)need;
+  const conv_status st = norm_check(d);
+  if (st != CONV_OK) return st;
   const int esz = d->dtype == CONV_F32 ? 4 : 2;
   if (((uintptr_t)x | (uintptr_t)y) & (esz - 1)) return CONV_E_ALIGN;
   if (((uintptr_t)gamma | (uintptr_t)beta | (uintptr_t)stats) & 3) return CONV_E_ALIGN;
+  const NormPlan plan = norm_plan(*d, false, std::min(align_of(x), align_of(y)));
+  const int64_t need = norm_ws_bytes(*d, plan, false);
+  if (need >= kMaxBytes) return CONV_E_UNSUPPORTED;
   if (need > 0 && !ws) return CONV_E_NULL;
   if ((uintptr_t)ws & 255) return CONV_E_ALIGN;
   if (need > ws_bytes) return CONV_E_SCRATCH;
@@ -224,7 +227,7 @@ conv_status conv_group_norm(const conv_norm_desc* d, const void* x, const float*
   a.y = y;
   a.stats = stats;
   a.part = static_cast<float*>(ws);
-  a.p = norm_plan(*d, false, std::min(align_of(x), align_of(y)));
+  a.p = plan;
   return hip_status(launch_norm(a, d->dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -232,12 +235,15 @@ conv_status conv_group_norm_grad(const conv_norm_desc* d, const void* x, const v
                                  const float* gamma, const float* beta, void* dx, float* dgamma, float* dbeta,
                                  void* ws, int64_t ws_bytes, void* stream) {
   if (!d || !x || !dy || !stats || !dx) return CONV_E_NULL;
-  const int64_t need = conv_group_norm_ws_bytes(d, 1);
-  if (need < 0) return (conv_status)need;
+  const conv_status st = norm_check(d);
+  if (st != CONV_OK) return st;
   const int esz = d->dtype == CONV_F32 ? 4 : 2;
   if (((uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx) & (esz - 1)) return CONV_E_ALIGN;
   if (((uintptr_t)gamma | (uintptr_t)beta | (uintptr_t)stats | (uintptr_t)dgamma | (uintptr_t)dbeta) & 3)
     return CONV_E_ALIGN;
+  const NormPlan plan = norm_plan(*d, true, std::min(align_of(x), std::min(align_of(dy), align_of(dx))));
+  const int64_t need = norm_ws_bytes(*d, plan, true);
+  if (need >= kMaxBytes) return CONV_E_UNSUPPORTED;
   if (need > 0 && !ws) return CONV_E_NULL;
   if ((uintptr_t)ws & 255) return CONV_E_ALIGN;
   if (need > ws_bytes) return CONV_E_SCRATCH;
@@ -255,11 +261,8 @@ conv_status conv_group_norm_grad(const conv_norm_desc* d, const void* x, const v
   a.stats = const_cast<float*>(stats);
   a.dgamma = dgamma;
   a.dbeta = dbeta;
-  a.p = norm_plan(*d, true, std::min(align_of(x), std::min(align_of(dy), align_of(dx))));
-  // ws: [n][c][2] totals, [n][groups][2] means, [n][chunks][c][2] chunk sums
-  a.tot = static_cast<float*>(ws);
-  a.means = a.tot + 2 * d->n * d->c;
-  a.part = a.means + 2 * d->n * d->groups;
+  a.p = plan;
+  a.part = static_cast<float*>(ws);
   return hip_status(launch_norm_grad(a, d->dtype, static_cast<hipStream_t>(stream)));
 }
 

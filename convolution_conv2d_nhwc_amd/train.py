@@ -11,6 +11,7 @@ them to the current stream, so a caller that passes another ``stream`` gives
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -70,39 +71,68 @@ def _L():
 
 
 def _dev(t: torch.Tensor, name: str, dt, shape):
+    if t.dtype is dt and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
     if t.dtype != dt:
         raise ValueError("%s dtype %s, expected %s" % (name, t.dtype, dt))
     if t.shape != shape:
         raise ValueError("%s shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _scratch(need: int, ws: Optional[torch.Tensor], device, what: str) -> Optional[torch.Tensor]:
-    """ws as given, or scratch of `need` bytes (a negative need is the
-    library's refusal of the description)."""
+def _like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _scratch(need: int, ws: Optional[torch.Tensor], t: torch.Tensor, what: str):
+    """(ws, its address, its bytes): ws as given, or scratch of `need` bytes
+    on t's device (a negative need is the library's refusal)."""
     if need < 0:
-        _lib._check(int(need), what)
-    if ws is not None:
-        if not ws.is_cuda or not ws.is_contiguous():
-            raise ValueError("ws must be a contiguous device tensor")
-        return ws
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        _lib._check(need, what)
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=t.device)
+        return ws, ws.data_ptr(), need
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous device tensor")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _ws_args(ws: Optional[torch.Tensor]) -> Tuple[Optional[int], int]:
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _stream(stream, t: torch.Tensor) -> int:
+    """The given stream's handle, or that of t's device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _lib._stream_handle(stream)
+
+
+def _need(need: int, what: str) -> int:
+    if need < 0:
+        _lib._check(need, what)
+    return need
+
+
+# The descriptions below and their scratch sizes depend on sizes and types
+# alone: they are computed once for each.
+_once = functools.lru_cache(maxsize=4096)
 
 
 # ------------------------------------------------------------------ group norm --
 
-def _norm_desc(x: torch.Tensor, groups: int, eps: float, act: str) -> _NormDesc:
+@_once
+def _norm_call(n, h, w, c, pitch, groups, dtype, act, eps, grad):
+    d = _NormDesc(n, h, w, c, pitch, groups, _FLOATS[dtype], NORM_ACTS[act], eps)
+    return d, int(_L().conv_group_norm_ws_bytes(d, int(grad)))
+
+
+def _norm_of(x: torch.Tensor, groups: int, eps: float, act: str, grad: bool):
+    """(description, scratch bytes) of the norm of x."""
     if x.dim() != 4 or x.dtype not in _FLOATS or not x.is_cuda:
         raise ValueError("x must be a [n, h, w, c] float32 or bfloat16 device tensor")
     if act not in NORM_ACTS:
@@ -111,11 +141,12 @@ def _norm_desc(x: torch.Tensor, groups: int, eps: float, act: str) -> _NormDesc:
     pitch = 0
     if not x.is_contiguous():
         # one step from pixel to pixel over the whole map: a channel slice of a wider NHWC map
-        pitch = x.stride(2) if w > 1 else x.stride(1) if h > 1 else x.stride(0) if n > 1 else c
-        if ((c > 1 and x.stride(3) != 1) or (w > 1 and x.stride(2) != pitch) or (h > 1 and x.stride(1) != w * pitch) or
-                (n > 1 and x.stride(0) != h * w * pitch)):
+        sn, sh, sw, sc = x.stride()
+        pitch = sw if w > 1 else sh if h > 1 else sn if n > 1 else c
+        if ((c > 1 and sc != 1) or (w > 1 and sw != pitch) or (h > 1 and sh != w * pitch) or
+                (n > 1 and sn != h * w * pitch)):
             raise ValueError("x must be NHWC with evenly spaced pixels (a contiguous map or a channel slice of one)")
-    return _NormDesc(n, h, w, c, pitch, groups, _FLOATS[x.dtype], NORM_ACTS[act], eps)
+    return _norm_call(n, h, w, c, pitch, groups, x.dtype, act, eps, grad)
 
 
 def _affine(gamma, beta, c):
@@ -126,10 +157,7 @@ def _affine(gamma, beta, c):
 
 def group_norm_ws_bytes(x: torch.Tensor, groups: int, eps: float = 1e-5, act: str = "none", grad: bool = False) -> int:
     """Bytes of ``ws`` that group_norm (or group_norm_grad) takes for x."""
-    need = _L().conv_group_norm_ws_bytes(_norm_desc(x, groups, eps, act), int(grad))
-    if need < 0:
-        _lib._check(int(need), "conv_group_norm_ws_bytes")
-    return int(need)
+    return _need(_norm_of(x, groups, eps, act, grad)[1], "conv_group_norm_ws_bytes")
 
 
 def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,
@@ -143,19 +171,19 @@ def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = Non
     wider map; gamma, beta float32 [c]; act "none", "relu", "relu6", "mish"
     or "silu". stats float32 [n, groups, 2] receives (mean, 1/sqrt(var + eps)),
     which group_norm_grad takes."""
-    L = _L()
-    d = _norm_desc(x, groups, eps, act)
+    d, need = _norm_of(x, groups, eps, act, False)
     _affine(gamma, beta, x.shape[3])
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _like(x)
     else:
         _dev(y, "y", x.dtype, x.shape)
     if stats is not None:
         _dev(stats, "stats", torch.float32, (x.shape[0], groups, 2))
-    ws = _scratch(L.conv_group_norm_ws_bytes(d, 0), ws, x.device, "conv_group_norm")
-    st = L.conv_group_norm(d, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(stats), *_ws_args(ws),
-                           _lib._stream_handle(stream))
-    _lib._check(st, "conv_group_norm")
+    ws, at, size = _scratch(need, ws, x, "conv_group_norm")
+    st = _L().conv_group_norm(d, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(stats), at, size,
+                              _stream(stream, x))
+    if st:
+        _lib._check(st, "conv_group_norm")
     return y
 
 
@@ -166,41 +194,51 @@ def group_norm_grad(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gamm
     """(dx, dgamma, dbeta) of group_norm for the upstream gradient dy (x's
     shape and dtype, contiguous), from the x, gamma, beta and act of the
     forward call and the stats it wrote."""
-    L = _L()
     if stats.dim() != 3:
         raise ValueError("stats must be [n, groups, 2]")
     groups = stats.shape[1]
-    d = _norm_desc(x, groups, 0.0, act)  # eps is in the stats
+    d, need = _norm_of(x, groups, 0.0, act, True)  # eps is in the stats
     c = x.shape[3]
     _dev(stats, "stats", torch.float32, (x.shape[0], groups, 2))
     _dev(dy, "dy", x.dtype, x.shape)
     _affine(gamma, beta, c)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = _like(x)
     else:
         _dev(dx, "dx", x.dtype, x.shape)
     if dgamma is None:
         dgamma = torch.empty(c, dtype=torch.float32, device=x.device)
+    else:
+        _dev(dgamma, "dgamma", torch.float32, (c,))
     if dbeta is None:
         dbeta = torch.empty(c, dtype=torch.float32, device=x.device)
-    _affine(dgamma, dbeta, c)
-    ws = _scratch(L.conv_group_norm_ws_bytes(d, 1), ws, x.device, "conv_group_norm_grad")
-    st = L.conv_group_norm_grad(d, x.data_ptr(), dy.data_ptr(), stats.data_ptr(), _ptr(gamma), _ptr(beta),
-                                dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), *_ws_args(ws),
-                                _lib._stream_handle(stream))
-    _lib._check(st, "conv_group_norm_grad")
+    else:
+        _dev(dbeta, "dbeta", torch.float32, (c,))
+    ws, at, size = _scratch(need, ws, x, "conv_group_norm_grad")
+    st = _L().conv_group_norm_grad(d, x.data_ptr(), dy.data_ptr(), stats.data_ptr(), _ptr(gamma), _ptr(beta),
+                                   dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), at, size, _stream(stream, x))
+    if st:
+        _lib._check(st, "conv_group_norm_grad")
     return dx, dgamma, dbeta
 
 
 # ------------------------------------------------------------------- head loss --
 
-def _head_desc(x, w, labels, weights) -> _HeadDesc:
+@_once
+def _head_call(rows, c, classes, label_bytes, grad):
+    d = _HeadDesc(rows, c, classes, _lib.DTYPES["bf16"], label_bytes)
+    return d, int(_L().conv_head_loss_ws_bytes(d, int(grad)))
+
+
+def _head_of(x, w, labels, weights, grad):
+    """(description, scratch bytes) of the loss of x under w."""
     if w.dim() == 4 and w.shape[1] == w.shape[2] == 1:
         classes, c = w.shape[0], w.shape[3]  # OHWI of a 1x1 layer
     elif w.dim() == 2:
         classes, c = w.shape
     else:
         raise ValueError("w must be [classes, c] (or OHWI [classes, 1, 1, c])")
+    pixels = x.shape[:-1]
     if x.dim() < 2 or x.shape[-1] != c:
         raise ValueError("x must be [..., c] with w's %d channels" % c)
     rows = x.numel() // c if c else 0
@@ -208,18 +246,15 @@ def _head_desc(x, w, labels, weights) -> _HeadDesc:
     _dev(w, "w", torch.bfloat16, w.shape)
     if labels.dtype not in (torch.int32, torch.int64):
         raise ValueError("labels must be int32 or int64")
-    _dev(labels, "labels", labels.dtype, x.shape[:-1])
+    _dev(labels, "labels", labels.dtype, pixels)
     if weights is not None:
-        _dev(weights, "weights", torch.float32, x.shape[:-1])
-    return _HeadDesc(rows, c, classes, _lib.DTYPES["bf16"], labels.element_size())
+        _dev(weights, "weights", torch.float32, pixels)
+    return _head_call(rows, c, classes, 8 if labels.dtype is torch.int64 else 4, grad)
 
 
 def head_loss_ws_bytes(rows: int, c: int, classes: int, grad: bool = False) -> int:
     """Bytes of ``ws`` that head_loss (or head_loss_grad) takes."""
-    need = _L().conv_head_loss_ws_bytes(_HeadDesc(rows, c, classes, _lib.DTYPES["bf16"], 8), int(grad))
-    if need < 0:
-        _lib._check(int(need), "conv_head_loss_ws_bytes")
-    return int(need)
+    return _need(_head_call(rows, c, classes, 8, bool(grad))[1], "conv_head_loss_ws_bytes")
 
 
 def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -229,13 +264,13 @@ def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weights: O
     under the 1x1 head w [classes, c] (both bfloat16) and its weighted sum,
     or mean when weights is None, as float32. labels [...] int32 or int64; a
     pixel whose label lies outside 0 .. classes-1 is left out."""
-    L = _L()
-    d = _head_desc(x, w, labels, weights)
+    d, need = _head_of(x, w, labels, weights, False)
     loss, total = _loss_outputs(x, loss, total)
-    ws = _scratch(L.conv_head_loss_ws_bytes(d, 0), ws, x.device, "conv_head_loss")
-    st = L.conv_head_loss(d, x.data_ptr(), w.data_ptr(), labels.data_ptr(), _ptr(weights), loss.data_ptr(),
-                          total.data_ptr(), *_ws_args(ws), _lib._stream_handle(stream))
-    _lib._check(st, "conv_head_loss")
+    ws, at, size = _scratch(need, ws, x, "conv_head_loss")
+    st = _L().conv_head_loss(d, x.data_ptr(), w.data_ptr(), labels.data_ptr(), _ptr(weights), loss.data_ptr(),
+                             total.data_ptr(), at, size, _stream(stream, x))
+    if st:
+        _lib._check(st, "conv_head_loss")
     return total, loss
 
 
@@ -257,22 +292,21 @@ def head_loss_grad(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weigh
                    ws: Optional[torch.Tensor] = None, stream=None):
     """(total, loss, dx, dw): head_loss and the gradients of total, bfloat16
     in the shapes of x and w."""
-    L = _L()
-    d = _head_desc(x, w, labels, weights)
+    d, need = _head_of(x, w, labels, weights, True)
     loss, total = _loss_outputs(x, loss, total)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(x)
     else:
         _dev(dx, "dx", x.dtype, x.shape)
     if dw is None:
-        dw = torch.empty(w.shape, dtype=w.dtype, device=w.device)
+        dw = torch.empty_like(w)
     else:
         _dev(dw, "dw", w.dtype, w.shape)
-    ws = _scratch(L.conv_head_loss_ws_bytes(d, 1), ws, x.device, "conv_head_loss_grad")
-    st = L.conv_head_loss_grad(d, x.data_ptr(), w.data_ptr(), labels.data_ptr(), _ptr(weights), loss.data_ptr(),
-                               total.data_ptr(), dx.data_ptr(), dw.data_ptr(), *_ws_args(ws),
-                               _lib._stream_handle(stream))
-    _lib._check(st, "conv_head_loss_grad")
+    ws, at, size = _scratch(need, ws, x, "conv_head_loss_grad")
+    st = _L().conv_head_loss_grad(d, x.data_ptr(), w.data_ptr(), labels.data_ptr(), _ptr(weights), loss.data_ptr(),
+                                  total.data_ptr(), dx.data_ptr(), dw.data_ptr(), at, size, _stream(stream, x))
+    if st:
+        _lib._check(st, "conv_head_loss_grad")
     return total, loss, dx, dw
 
 
@@ -281,25 +315,16 @@ def head_loss_grad(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weigh
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
 
 
-def _ortho_desc(g, steps, coeffs, eps) -> _OrthoDesc:
-    if g.dim() < 2 or g.dtype not in _FLOATS:
-        raise ValueError("g must be float32 or bfloat16, [m, n], [batch, m, n] or OHWI [c_out, kh, kw, c_in]")
-    _dev(g, "g", g.dtype, g.shape)
-    if g.dim() == 3:
-        batch, rows, cols = g.shape
-    else:
-        batch, rows = 1, g.shape[0]
-        cols = g.numel() // rows if rows else 0
-    a, b, c = coeffs
-    return _OrthoDesc(batch, rows, cols, _FLOATS[g.dtype], steps, a, b, c, eps)
+@_once
+def _ortho_call(batch, rows, cols, dtype, steps, a, b, c, eps):
+    d = _OrthoDesc(batch, rows, cols, _FLOATS[dtype], steps, a, b, c, eps)
+    return d, int(_L().conv_orthogonalize_ws_bytes(d))
 
 
 def orthogonalize_ws_bytes(batch: int, rows: int, cols: int) -> int:
     """Bytes of ``ws`` that orthogonalize takes for [batch, rows, cols]."""
-    need = _L().conv_orthogonalize_ws_bytes(_OrthoDesc(batch, rows, cols, 0, 1, 1.0, 0.0, 0.0, 0.0))
-    if need < 0:
-        _lib._check(int(need), "conv_orthogonalize_ws_bytes")
-    return int(need)
+    return _need(_ortho_call(batch, rows, cols, torch.float32, 1, 1.0, 0.0, 0.0, 0.0)[1],
+                 "conv_orthogonalize_ws_bytes")
 
 
 def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = MUON_COEFFS, eps: float = 1e-7,
@@ -307,13 +332,23 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = MUO
     """The Newton-Schulz orthogonalisation of g, bfloat16 in g's shape: g
     [m, n], a batch [b, m, n] of matrices, or one layer's OHWI weight gradient
     [c_out, kh, kw, c_in] as the matrix [c_out, kh kw c_in]."""
-    L = _L()
-    d = _ortho_desc(g, steps, coeffs, eps)
-    if out is None:
-        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    if g.dim() < 2 or g.dtype not in _FLOATS:
+        raise ValueError("g must be float32 or bfloat16, [m, n], [batch, m, n] or OHWI [c_out, kh, kw, c_in]")
+    shape = g.shape
+    _dev(g, "g", g.dtype, shape)
+    if len(shape) == 3:
+        batch, rows, cols = shape
     else:
-        _dev(out, "out", torch.bfloat16, g.shape)
-    ws = _scratch(L.conv_orthogonalize_ws_bytes(d), ws, g.device, "conv_orthogonalize")
-    st = L.conv_orthogonalize(d, g.data_ptr(), out.data_ptr(), *_ws_args(ws), _lib._stream_handle(stream))
-    _lib._check(st, "conv_orthogonalize")
+        batch, rows = 1, shape[0]
+        cols = g.numel() // rows if rows else 0
+    a, b, c = coeffs
+    d, need = _ortho_call(batch, rows, cols, g.dtype, steps, a, b, c, eps)
+    if out is None:
+        out = torch.empty_like(g, dtype=torch.bfloat16)
+    else:
+        _dev(out, "out", torch.bfloat16, shape)
+    ws, at, size = _scratch(need, ws, g, "conv_orthogonalize")
+    st = _L().conv_orthogonalize(d, g.data_ptr(), out.data_ptr(), at, size, _stream(stream, g))
+    if st:
+        _lib._check(st, "conv_orthogonalize")
     return out
