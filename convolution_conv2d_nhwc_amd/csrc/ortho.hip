@@ -127,6 +127,18 @@ __global__ __launch_bounds__(256) void start_kernel(const T* g, Layout l, const 
   }
 }
 
+// `left` of the four values, as one vector where rows allow
+__device__ __forceinline__ void put4(uint16_t* o, uint2 v, int left, int vec) {
+  if (vec && left >= 4) {
+    *reinterpret_cast<uint2*>(o) = v;
+  } else {
+    if (left > 0) o[0] = (uint16_t)v.x;
+    if (left > 1) o[1] = (uint16_t)(v.x >> 16);
+    if (left > 2) o[2] = (uint16_t)v.y;
+    if (left > 3) o[3] = (uint16_t)(v.y >> 16);
+  }
+}
+
 // Stores v (four consecutive q of row p) to out[p][q], and where `both` to
 // out[q][p]: pitch mp, in bounds for p, q < mp (multiples of 64, as 16-wide
 // fragments are whole).
@@ -331,17 +343,6 @@ struct StepEpi {
       });
     });
   }
-  // `left` of the four values, as one vector where rows allow
-  static __device__ __forceinline__ void put4(uint16_t* o, uint2 v, int left, int vec) {
-    if (vec && left >= 4) {
-      *reinterpret_cast<uint2*>(o) = v;
-    } else {
-      if (left > 0) o[0] = (uint16_t)v.x;
-      if (left > 1) o[1] = (uint16_t)(v.x >> 16);
-      if (left > 2) o[2] = (uint16_t)v.y;
-      if (left > 3) o[3] = (uint16_t)(v.y >> 16);
-    }
-  }
 };
 
 Layout layout_of(int64_t rows, int64_t cols) {
@@ -354,12 +355,265 @@ Layout layout_of(int64_t rows, int64_t cols) {
   return l;
 }
 
+// ---- small matrices: everything in one launch ---------------------------------------
+
+// m <= 64 and n <= 1024 in one workgroup of 16 waves per matrix, all in LDS and
+// registers: 64 x 576 takes SMALLUS us against 78 in 17 launches. X lives in fp32
+// in the lanes that compute it (up to four blocks of 16 columns a wave, in the
+// MFMA result's layout: p = lane % 16 of four row blocks, four consecutive
+// columns) and in fp16 in LDS for the products; O and R as above. Of A and A A
+// ten waves compute one 16 x 16 block of the lower triangle each and store
+// both halves. Rows in LDS are 16 bytes longer than their values, so that the 16
+// rows of one read fall on different banks.
+constexpr int kSmallM = 64, kSmallN = 1024, kSmallWaves = 16;
+constexpr int kSmallPitch = kSmallM + 8;                  // of O and R, in values
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+__device__ __forceinline__ f32x4 mfma_f16(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// The exponent of a finite v > 0, else 0 (infinities and NaN stay themselves).
+__device__ __forceinline__ int ilogb_f64(double v) {
+  return v > 0.0 && v < __builtin_inf() ? __builtin_amdgcn_frexp_exp(v) - 1 : 0;
+}
+
+// Four values of G from i on; vec: as one load.
+template <typename T>
+__device__ __forceinline__ f32x4 g_at4(const T* g, int64_t i, int left, bool vec) {
+  f32x4 v = {0, 0, 0, 0};
+  if (vec) {
+    if (left > 0) {
+      if constexpr (sizeof(T) == 4) {
+        v = *reinterpret_cast<const f32x4*>(g + i);
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(g + i);
+        v = f32x4{bf16_bits_to_f32(u.x & 0xffffu), bf16_bits_to_f32(u.x >> 16), bf16_bits_to_f32(u.y & 0xffffu),
+                  bf16_bits_to_f32(u.y >> 16)};
+      }
+    }
+  } else {
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      if (z < left) v[z] = g_at(g, i + z);
+  }
+  return v;
+}
+
+// NB: column blocks per wave. in_vec, out_vec: G (not tall) and out take vectors of four.
+template <typename T, int NB>
+__global__ __launch_bounds__(64 * kSmallWaves) void small_kernel(const T* g, uint16_t* out, Layout l, int steps,
+                                                                 float ca, float cb, float cc, float eps, int in_vec,
+                                                                 int out_vec) {
+  __shared__ __attribute__((aligned(16))) _Float16 x[kSmallM * (kSmallN + 8)];
+  __shared__ __attribute__((aligned(16))) _Float16 o[kSmallM * kSmallPitch], r[kSmallM * kSmallPitch];
+  __shared__ __attribute__((aligned(16))) float d[kSmallM], e[kSmallM];
+  __shared__ double red[kSmallWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lp = lane & 15, lq = 4 * (lane >> 4), lk = 8 * (lane >> 4);
+  const int pitch = l.np + 8;  // of x
+  const int64_t mat = (int64_t)blockIdx.x * l.m * l.n;
+  const int nb = l.np / 16;
+
+  // block u of the wave: columns 16 (wave + 16 u) ..
+  f32x4 xr[NB][4];
+  double sq = 0.0;
+#pragma unroll
+  for (int u = 0; u < NB; ++u) {
+    const int q = 16 * (wave + kSmallWaves * u) + lq;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = 16 * i + lp;
+      f32x4 v = {0, 0, 0, 0};
+      if (p < l.m) {
+        if (l.tall) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            if (q + z < l.n) v[z] = g_at(g, mat + (int64_t)(q + z) * l.m + p);
+        } else {
+          v = g_at4(g, mat + (int64_t)p * l.n + q, l.n - q, in_vec);
+        }
+      }
+      xr[u][i] = v;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < NB; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int z = 0; z < 4; ++z) sq += (double)xr[u][i][z] * xr[u][i][z];
+#pragma unroll
+  for (int k = 32; k >= 1; k >>= 1) sq += __shfl_xor(sq, k);
+  if (lane == 0) red[wave] = sq;
+  __syncthreads();
+  sq = 0.0;
+#pragma unroll
+  for (int k = 0; k < kSmallWaves; ++k) sq += red[k];
+  // as inv_m 2^inv_k: the factor for a tiny G would leave fp32's range
+  const double inv = (double)kSx / (sqrt(sq) + (double)eps);
+  const int inv_k = ilogb_f64(inv);
+  const float inv_m = (float)__builtin_ldexp(inv, -inv_k);
+
+  auto put_x = [&]() {
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const int b = wave + kSmallWaves * u;
+      if (b < nb) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint2*>(x + (16 * i + lp) * pitch + 16 * b + lq) =
+              uint2{half2_bits(xr[u][i][0], xr[u][i][1]), half2_bits(xr[u][i][2], xr[u][i][3])};
+      }
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < NB; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int z = 0; z < 4; ++z) xr[u][i][z] = __builtin_ldexpf(xr[u][i][z] * inv_m, inv_k);
+  put_x();
+  // the wave's block of the lower triangle: pb (pb + 1) / 2 + qb = wave
+  int pb = 0, qb = wave;
+  while (qb > pb) {
+    ++pb;
+    qb -= pb;
+  }
+  const bool tri = wave < 10;
+  // 16 x 16 values of a symmetric 64 x 64 matrix, both ways round
+  auto put_both = [&](_Float16* to, const float (&f)[4]) {
+    const int p = 16 * pb + lp, q = 16 * qb + lq;
+    const uint2 v = {half2_bits(f[0], f[1]), half2_bits(f[2], f[3])};
+    *reinterpret_cast<uint2*>(to + p * kSmallPitch + q) = v;
+    if (pb != qb)
+      *reinterpret_cast<uint2*>(to + (q + (lane & 3)) * kSmallPitch + (p & ~3)) = quad_transpose(v, lane);
+  };
+  __syncthreads();
+
+  for (int step = 0; step < steps; ++step) {
+    if (tri) {  // A = X X^T
+      const _Float16* xa = x + (16 * qb + lp) * pitch + lk;
+      const _Float16* xb = x + (16 * pb + lp) * pitch + lk;
+      f32x4 a0 = {0, 0, 0, 0}, a1 = {0, 0, 0, 0};
+#pragma unroll 4
+      for (int k = 0; k < l.np; k += 64) {
+        a0 = mfma_f16(*reinterpret_cast<const f16x8*>(xa + k), *reinterpret_cast<const f16x8*>(xb + k), a0);
+        a1 = mfma_f16(*reinterpret_cast<const f16x8*>(xa + k + 32), *reinterpret_cast<const f16x8*>(xb + k + 32), a1);
+      }
+      float f[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        f[z] = (a0[z] + a1[z]) * (kSo / (kSx * kSx));
+        if (pb == qb && lp == lq + z) {
+          d[16 * pb + lp] = f[z] * (1.0f / kSo);
+          f[z] = 0.0f;
+        }
+      }
+      put_both(o, f);
+    }
+    __syncthreads();
+    if (tri) {  // Q = a I + b A + c A A
+      f32x4 a0 = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < kSmallM; k += 32)
+        a0 = mfma_f16(*reinterpret_cast<const f16x8*>(o + (16 * qb + lp) * kSmallPitch + lk + k),
+                      *reinterpret_cast<const f16x8*>(o + (16 * pb + lp) * kSmallPitch + lk + k), a0);
+      const int p = 16 * pb + lp, q = 16 * qb + lq;
+      float of[4], f[4];
+      half4(*reinterpret_cast<const uint2*>(o + p * kSmallPitch + q), of);
+      const float dp = d[p];
+      const f32x4 dq = *reinterpret_cast<const f32x4*>(d + q);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const float oo = a0[z] * (1.0f / (kSo * kSo)), ov = of[z] * (1.0f / kSo);
+        f[z] = (cb * ov + cc * (oo + (dp + dq[z]) * ov)) * kSr;
+        if (p == q + z) {
+          e[p] = ca + cb * dp + cc * (oo + dp * dp);
+          f[z] = 0.0f;
+        }
+      }
+      put_both(r, f);
+    }
+    __syncthreads();
+    // X <- E_p X_p + R X, the wave's own columns, two row blocks at a time (registers)
+#pragma unroll
+    for (int h = 0; h < 4; h += 2) {
+      f16x8 rf[2][2];
+      float ep[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ep[i] = e[16 * (h + i) + lp];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          rf[i][k] = *reinterpret_cast<const f16x8*>(r + (16 * (h + i) + lp) * kSmallPitch + lk + 32 * k);
+      }
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        const int b = wave + kSmallWaves * u;
+        if (b < nb) {
+          f16x8 xt[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const _Float16* at = x + (32 * k + lk + ((lane >> 2) & 3)) * pitch + 16 * b + 4 * (lane & 3);
+            struct {
+              s16x4 lo, hi;
+            } v;
+            v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+            v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * pitch));
+            xt[k] = __builtin_bit_cast(f16x8, v);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            f32x4 a0 = {0, 0, 0, 0};
+            a0 = mfma_f16(xt[0], rf[i][0], a0);
+            a0 = mfma_f16(xt[1], rf[i][1], a0);
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              xr[u][h + i][z] = ep[i] * xr[u][h + i][z] + a0[z] * (1.0f / kSr);
+          }
+        }
+      }
+    }
+    // a wave reads and writes its own columns of x only, and the next step's
+    // product reads it behind the barrier
+    if (step + 1 < steps) {
+      put_x();
+      __syncthreads();
+    }
+  }
+
+#pragma unroll
+  for (int u = 0; u < NB; ++u) {
+    const int q = 16 * (wave + kSmallWaves * u) + lq;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = 16 * i + lp;
+      float f[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) f[z] = xr[u][i][z] * (1.0f / kSx);
+      if (l.tall) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (p < l.m && q + z < l.n) out[mat + (int64_t)(q + z) * l.m + p] = f32_to_bf16_bits(f[z]);
+      } else if (p < l.m && q < l.n) {
+        put4(out + mat + (int64_t)p * l.n + q, uint2{bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3])}, l.n - q,
+             out_vec);
+      }
+    }
+  }
+}
+
 struct OrthoWs {
   int64_t part, hi0, hi1, lo, o, r, d, e, bytes;
 };
 
+// ws.bytes is 0 for matrices that small_kernel takes
 OrthoWs ortho_layout(int64_t batch, const Layout& l) {
-  OrthoWs w;
+  OrthoWs w = {};
+  if (l.mp <= kSmallM && l.np <= kSmallN) return w;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -393,13 +647,40 @@ hipError_t launch_start(const OrthoArgs& a, const Layout& l, const OrthoWs& w, h
   return hipGetLastError();
 }
 
+template <typename T, int NB>
+void launch_small_nb(const OrthoArgs& a, const Layout& l, int out_vec, hipStream_t s) {
+  const T* g = static_cast<const T*>(a.g);
+  const int in_vec = !l.tall && l.n % 4 == 0 && ((uintptr_t)g & (4 * sizeof(T) - 1)) == 0;
+  hipLaunchKernelGGL((small_kernel<T, NB>), dim3(a.batch), dim3(64 * kSmallWaves), 0, s, g, a.out, l, a.steps, a.a,
+                     a.b, a.c, a.eps, in_vec, out_vec);
+}
+
+template <typename T>
+void launch_small(const OrthoArgs& a, const Layout& l, int out_vec, hipStream_t s) {
+  switch (cdiv(l.np, 16 * kSmallWaves)) {
+    case 1: return launch_small_nb<T, 1>(a, l, out_vec, s);
+    case 2: return launch_small_nb<T, 2>(a, l, out_vec, s);
+    case 3: return launch_small_nb<T, 3>(a, l, out_vec, s);
+    default: return launch_small_nb<T, 4>(a, l, out_vec, s);
+  }
+}
+
 }  // namespace
 
 int64_t ortho_ws_bytes(const conv_ortho_desc& d) { return ortho_layout(d.batch, layout_of(d.rows, d.cols)).bytes; }
 
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   const Layout l = layout_of(a.rows, a.cols);
+  const int out_row = l.tall ? l.m : l.n;
+  const int out_vec = out_row % 4 == 0 && ((uintptr_t)a.out & 7) == 0;
   const OrthoWs w = ortho_layout(a.batch, l);
+  if (!w.bytes) {
+    if (a.g_f32)
+      launch_small<float>(a, l, out_vec, s);
+    else
+      launch_small<uint16_t>(a, l, out_vec, s);
+    return hipGetLastError();
+  }
   hipError_t err = a.g_f32 ? launch_start<float>(a, l, w, s) : launch_start<uint16_t>(a, l, w, s);
   if (err != hipSuccess) return err;
   _Float16* lo = reinterpret_cast<_Float16*>(a.ws + w.lo);
@@ -409,8 +690,6 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   float* e = reinterpret_cast<float*>(a.ws + w.e);
   const int sym_tile = gemm_tile(l.mp, l.mp, a.batch, true);
   const int step_tile = gemm_tile(l.np, l.mp, a.batch, false);
-  const int out_row = l.tall ? l.m : l.n;
-  const int out_vec = out_row % 4 == 0 && ((uintptr_t)a.out & 7) == 0;
   for (int k = 0; k < a.steps; ++k) {
     const bool last = k + 1 == a.steps;
     _Float16* hi = reinterpret_cast<_Float16*>(a.ws + (k % 2 ? w.hi1 : w.hi0));

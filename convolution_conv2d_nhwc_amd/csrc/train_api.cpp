@@ -170,9 +170,10 @@ int64_t conv_orthogonalize_ws_bytes(const conv_ortho_desc* d) {
 
 conv_status conv_orthogonalize(const conv_ortho_desc* d, const void* g, void* out, void* ws, int64_t ws_bytes,
                                void* stream) {
-  if (!d || !g || !out || !ws) return CONV_E_NULL;
+  if (!d || !g || !out) return CONV_E_NULL;
   const int64_t need = conv_orthogonalize_ws_bytes(d);
   if (need < 0) return (conv_status)need;
+  if (need > 0 && !ws) return CONV_E_NULL;
   const int64_t esz = d->dtype == CONV_F32 ? 4 : 2, count = d->batch * d->rows * d->cols;
   if ((uintptr_t)g & (esz - 1) || (uintptr_t)out & 1 || (uintptr_t)ws & 255) return CONV_E_ALIGN;
   if (need > ws_bytes) return CONV_E_SCRATCH;
