@@ -253,13 +253,13 @@ struct Cut {
   static constexpr int FP = kSplitK ? 1 : NF;      // the epilogue's accumulators: [NF][FP]
 };
 
+// One tile of a product: the workgroup `block` of nwg.
 template <int DT, int T, bool DEEP, bool KSA, bool KSB, class Epi>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DEEP ? 1 : 2, DEEP ? 1 : 2))) void
-gemm_kernel(GemmArgs g, typename Epi::Args e) {
+__device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename Epi::Args& e, char* smem, int block,
+                                              int nwg) {
   typedef Cut<T, DEEP> C;
   constexpr int F = C::NF, NMF = F * F, NST = C::NST, CH = C::CH, TILE = C::TILE, STAGE = C::STAGE, SUB = C::SUB;
   constexpr int NL = T / 32;  // loads per lane per K-tile and operand
-  __shared__ __attribute__((aligned(16))) char smem[NST * STAGE];
   const lds_ptr lds = (lds_ptr)smem;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -268,11 +268,11 @@ gemm_kernel(GemmArgs g, typename Epi::Args e) {
   at.split = blockIdx.y;
   at.batch = blockIdx.z;
 
-  // Each XCD (blockIdx.x % 8 under round-robin dispatch) walks a contiguous
+  // Each XCD (block % 8 under round-robin dispatch) walks a contiguous
   // run of tiles, `group` q tiles by all p tiles at a time, so that its L2
   // holds the rows it re-reads.
-  const int nwg = gridDim.x, xcd = blockIdx.x & 7;
-  const int lin = xcd * (nwg >> 3) + min(xcd, nwg & 7) + (blockIdx.x >> 3);
+  const int xcd = block & 7;
+  const int lin = xcd * (nwg >> 3) + min(xcd, nwg & 7) + (block >> 3);
   int qt, pt;
   at.mirror = false;
   if constexpr (Epi::kSymmetric) {
@@ -551,27 +551,61 @@ gemm_kernel(GemmArgs g, typename Epi::Args e) {
   }
 }
 
+template <int DT, int T, bool DEEP, bool KSA, bool KSB, class Epi>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DEEP ? 1 : 2, DEEP ? 1 : 2))) void
+gemm_kernel(GemmArgs g, typename Epi::Args e) {
+  __shared__ __attribute__((aligned(16))) char smem[Cut<T, DEEP>::NST * Cut<T, DEEP>::STAGE];
+  gemm_tile_run<DT, T, DEEP, KSA, KSB, Epi>(g, e, smem, blockIdx.x, gridDim.x);
+}
+
+// Two products that do not wait for each other in one launch: the first n0
+// workgroups run P0's, the others P1's. P: { KSA, KSB, Epi }.
+template <int DT, int T, class P0, class P1>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void
+gemm_pair_kernel(GemmArgs g0, typename P0::Epi::Args e0, int n0, GemmArgs g1, typename P1::Epi::Args e1) {
+  __shared__ __attribute__((aligned(16))) char smem[Cut<T, true>::NST * Cut<T, true>::STAGE];
+  if ((int)blockIdx.x < n0)
+    gemm_tile_run<DT, T, true, P0::KSA, P0::KSB, typename P0::Epi>(g0, e0, smem, blockIdx.x, n0);
+  else
+    gemm_tile_run<DT, T, true, P1::KSA, P1::KSB, typename P1::Epi>(g1, e1, smem, blockIdx.x - n0, gridDim.x - n0);
+}
+
 // ---- host side --------------------------------------------------------------
 
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-template <int DT, int T, bool DEEP, bool KSA, bool KSB, class Epi>
-hipError_t gemm_launch_t(GemmArgs g, const typename Epi::Args& e, int splits, int batch, hipStream_t s) {
-  const int nq = cdiv(g.q, T), np = cdiv(g.p, T);
-  g.nq = nq;
-  // the 32 or 64 tiles that an XCD works on together make a block that is about
-  // as wide as high: fewest rows fetched into its L2
-  g.group = std::min(nq, T == 256 ? 6 : 8);
-  g.kt_per = cdiv(cdiv(g.k, kKV), splits);
-  const int tiles = Epi::kSymmetric ? np * (np + 1) / 2 : nq * np;
-  hipLaunchKernelGGL((gemm_kernel<DT, T, DEEP, KSA, KSB, Epi>), dim3(tiles, splits, batch), dim3(256), 0, s, g, e);
-  return hipGetLastError();
-}
 
 // Workgroups of a product with tiles of side t.
 inline int64_t gemm_tiles(int64_t q, int64_t p, int t, bool symmetric) {
   const int64_t a = cdiv(q, t), b = cdiv(p, t);
   return symmetric ? a * (a + 1) / 2 : a * b;
+}
+
+// The tile order and the K-tiles per split.
+inline void gemm_order(GemmArgs& g, int t, int splits) {
+  g.nq = cdiv(g.q, t);
+  // the 32 or 64 tiles that an XCD works on together make a block that is about
+  // as wide as high: fewest rows fetched into its L2
+  g.group = std::min(g.nq, t == 256 ? 6 : 8);
+  g.kt_per = cdiv(cdiv(g.k, kKV), splits);
+}
+
+template <int DT, int T, bool DEEP, bool KSA, bool KSB, class Epi>
+hipError_t gemm_launch_t(GemmArgs g, const typename Epi::Args& e, int splits, int batch, hipStream_t s) {
+  gemm_order(g, T, splits);
+  const int tiles = (int)gemm_tiles(g.q, g.p, T, Epi::kSymmetric);
+  hipLaunchKernelGGL((gemm_kernel<DT, T, DEEP, KSA, KSB, Epi>), dim3(tiles, splits, batch), dim3(256), 0, s, g, e);
+  return hipGetLastError();
+}
+
+// Both in tiles of T, unsplit.
+template <int DT, int T, class P0, class P1>
+hipError_t gemm_launch_pair(GemmArgs g0, const typename P0::Epi::Args& e0, GemmArgs g1,
+                            const typename P1::Epi::Args& e1, hipStream_t s) {
+  gemm_order(g0, T, 1);
+  gemm_order(g1, T, 1);
+  const int n0 = (int)gemm_tiles(g0.q, g0.p, T, false), n1 = (int)gemm_tiles(g1.q, g1.p, T, false);
+  hipLaunchKernelGGL((gemm_pair_kernel<DT, T, P0, P1>), dim3(n0 + n1), dim3(256), 0, s, g0, e0, n0, g1, e1);
+  return hipGetLastError();
 }
 
 // Tile: 256 when that fills the chip (one workgroup a CU), else 128 when it

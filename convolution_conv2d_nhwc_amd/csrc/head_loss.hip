@@ -74,6 +74,22 @@ __global__ __launch_bounds__(256) void pad_kernel(const uint16_t* x, int64_t nx,
   }
 }
 
+// What an epilogue reads of a row (one p), besides the accumulators: before
+// the product where a lane has one row.
+template <int FP, class Epi>
+struct RowPre {
+  typename Epi::Row first;
+  __device__ __forceinline__ void load(const TileAt& at, const typename Epi::Args& e) {
+    if constexpr (FP == 1) first.load(at, e, 0);
+  }
+  __device__ __forceinline__ typename Epi::Row row(const TileAt& at, const typename Epi::Args& e, int j) const {
+    if constexpr (FP == 1) return first;
+    typename Epi::Row r;
+    r.load(at, e, j);
+    return r;
+  }
+};
+
 // ---- forward ----------------------------------------------------------------------
 
 struct StatEpi {
@@ -84,17 +100,26 @@ struct StatEpi {
     const void* labels;
     int label_bytes, rows, classes, slots;
   };
+  struct Row {
+    int label;
+    __device__ __forceinline__ void load(const TileAt& at, const Args& e, int j) {
+      const int r = at.p0 + 16 * j;
+      label = r < e.rows ? label_at(e.labels, e.label_bytes, r, e.classes) : -1;
+    }
+  };
   template <int FQ, int FP>
-  using Pre = NoPre;
+  using Pre = RowPre<FP, StatEpi>;
   template <int FQ, int FP>
-  static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e, NoPre) {
+  static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e,
+                                             const Pre<FQ, FP>& pre) {
     if (at.wq + 16 * FQ > e.classes)
-      rows_of<FQ, FP, true>(acc, at, e);
+      rows_of<FQ, FP, true>(acc, at, e, pre);
     else
-      rows_of<FQ, FP, false>(acc, at, e);
+      rows_of<FQ, FP, false>(acc, at, e, pre);
   }
   template <int FQ, int FP, bool RAGGED>
-  static __device__ __forceinline__ void rows_of(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e) {
+  static __device__ __forceinline__ void rows_of(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e,
+                                                 const Pre<FQ, FP>& pre) {
     const int slot = at.wq / (16 * FQ);
     StaticFor<0, FP>::run([&](auto jc) {
       constexpr int j = decltype(jc)::value;
@@ -120,7 +145,7 @@ struct StatEpi {
       if (r < e.rows) {
         if (at.lane < 16) e.stat[(int64_t)r * e.slots + slot] = float2{m == -INFINITY ? m : base, s};
         // the label's logit, where it is one of this lane's: q0 + 16 i + 0..3
-        const int d = label_at(e.labels, e.label_bytes, r, e.classes) - at.q0;
+        const int d = pre.row(at, e, j).label - at.q0;
         if (d >= 0 && d < 16 * FQ && (d & 15) < 4) {
           float u = 0.0f;
 #pragma unroll
@@ -302,26 +327,35 @@ struct GradEpi {
     float* delta;        // [rows]
     int64_t vp;
   };
+  // rows past the last and rows left out: logits 0, lse 0, weight 0
+  struct Row {
+    float lse, k;
+    int d;  // the label, from the wave's first class
+    __device__ __forceinline__ void load(const TileAt& at, const Args& e, int j) {
+      const int r = at.p0 + 16 * j;
+      lse = k = 0.0f;
+      d = -1;
+      if (r >= e.rows) return;
+      const int lab = label_at(e.labels, e.label_bytes, r, e.classes);
+      lse = e.lse[r];
+      if (lab >= 0) {
+        k = e.weights ? e.weights[r] : e.inv[0];
+        d = lab - e.v0 - at.wq;
+      }
+    }
+  };
   template <int FQ, int FP>
-  using Pre = NoPre;
+  using Pre = RowPre<FP, GradEpi>;
   template <int FQ, int FP>
-  static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e, NoPre) {
+  static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e,
+                                             const Pre<FQ, FP>& pre) {
     const bool ragged = at.wq + 16 * FQ > e.nv;
-    const float inv = e.weights ? 0.0f : e.inv[0];
     StaticFor<0, FP>::run([&](auto jc) {
       constexpr int j = decltype(jc)::value;
       const int r = at.p0 + 16 * j;
-      // rows past the last and rows left out: logits 0, lse 0, weight 0
-      float lse = 0.0f, k = 0.0f;
-      int d = -1;  // the label, from the wave's first class
-      if (r < e.rows) {
-        const int lab = label_at(e.labels, e.label_bytes, r, e.classes);
-        lse = e.lse[r];
-        if (lab >= 0) {
-          k = e.weights ? e.weights[r] : inv;
-          d = lab - e.v0 - at.wq;
-        }
-      }
+      const Row in = pre.row(at, e, j);
+      const float lse = in.lse, k = in.k;
+      int d = in.d;
       uint16_t* const row = e.ds + (int64_t)r * e.vp + at.q0;
       if (ragged || __any(d >= 0 && d < 16 * FQ)) {
         d -= at.q0 - at.wq;
@@ -464,6 +498,15 @@ struct PartEpi {
   }
 };
 
+struct DxProduct {
+  static constexpr bool KSA = true, KSB = false;
+  typedef StoreEpi<true> Epi;
+};
+struct DwProduct {
+  static constexpr bool KSA = true, KSB = true;
+  typedef StoreEpi<false> Epi;
+};
+
 // out [rows][c] bf16 = the splits' sums, added in split order.
 __global__ __launch_bounds__(256) void part_sum_kernel(const float* part, int64_t split_stride, int splits,
                                                        int64_t rows, int c, int cq, uint16_t* out, int vec) {
@@ -491,14 +534,15 @@ __global__ __launch_bounds__(256) void part_sum_kernel(const float* part, int64_
 }
 
 // Tile and splits of a product: whole reductions where the tiles fill the
-// chip, else splits of at least 8 K-tiles (512 values of K).
+// chip, else splits of at least 8 K-tiles (512 values of K), as many as make
+// two rounds of 256 tiles or one of smaller ones.
 GemmShape shape_for(int64_t q, int64_t p, int64_t k) {
   auto tiles = [&](int t) { return (int64_t)cdiv(q, t) * cdiv(p, t); };
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplit, k / 512));
   if (tiles(256) >= 192) return {256, 1};
-  if (tiles(256) * most >= 192) return {256, (int)std::min<int64_t>(most, cdiv(512, tiles(256)))};
-  if (tiles(128) * most >= 128) return {128, (int)std::min<int64_t>(most, cdiv(256, tiles(128)))};
-  return {64, (int)std::min<int64_t>(most, cdiv(512, tiles(64)))};
+  if (tiles(256) * most >= 192) return {256, (int)std::min<int64_t>(most, std::max<int64_t>(1, 512 / tiles(256)))};
+  if (tiles(128) * most >= 128) return {128, (int)std::min<int64_t>(most, std::max<int64_t>(1, 256 / tiles(128)))};
+  return {64, (int)std::min<int64_t>(most, std::max<int64_t>(1, 256 / tiles(64)))};
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -537,6 +581,9 @@ HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w)
     p.ds_tile = gemm_tile(pv, rows, 1, false);
     p.dx = shape_for(c, rows, pv);
     p.dw = shape_for(c, pv, rows);
+    // short products in few tiles: both in one launch
+    p.pair = !pieces && p.dx.tile == 64 && p.dw.tile == 64 && p.dw.splits == 1 && pv <= 2048;
+    if (p.pair) p.dx.splits = 1;
     p.o_ds = take(rows * p.vp * 2);
     if (pieces || p.dx.splits > 1) p.o_dxp = take(p.dx.splits * rows * p.cq * 4);
     if (p.dw.splits > 1) p.o_dwp = take(p.dw.splits * pv * p.cq * 4);
@@ -645,13 +692,6 @@ hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s) {
     gx.k = (int)nv;
     gx.q = (int)p.cpad;
     gx.p = (int)a.rows;
-    if (p.o_dxp >= 0) {
-      const PartEpi<true>::Args pe = {f32_at(p.o_dxp), dx_stride, (int)a.rows, (int)p.cq, v0 > 0, lt, st};
-      CONV_TRY((gemm_launch<BF16, true, false, PartEpi<true>>(gx, pe, p.dx.tile, p.dx.splits, 1, s)));
-    } else {
-      const StoreEpi<true>::Args ee = {a.dx, (int)a.rows, (int)a.c, vec_dx, lt, st};
-      CONV_TRY((gemm_launch<BF16, true, false, StoreEpi<true>>(gx, ee, p.dx.tile, 1, 1, s)));
-    }
     // dw of the piece [nv][c] = g^T x
     GemmArgs gw = {};
     gw.a = reinterpret_cast<const char*>(xc);
@@ -662,6 +702,19 @@ hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s) {
     gw.q = (int)p.cpad;
     gw.p = (int)up(nv, 8);
     uint16_t* dw = a.dw + v0 * a.c;
+    if (p.pair) {
+      const StoreEpi<true>::Args ex = {a.dx, (int)a.rows, (int)a.c, vec_dx, lt, st};
+      const StoreEpi<false>::Args ew = {dw, (int)nv, (int)a.c, vec_dw, lt, st};
+      CONV_TRY((gemm_launch_pair<BF16, 64, DxProduct, DwProduct>(gx, ex, gw, ew, s)));
+      continue;
+    }
+    if (p.o_dxp >= 0) {
+      const PartEpi<true>::Args pe = {f32_at(p.o_dxp), dx_stride, (int)a.rows, (int)p.cq, v0 > 0, lt, st};
+      CONV_TRY((gemm_launch<BF16, true, false, PartEpi<true>>(gx, pe, p.dx.tile, p.dx.splits, 1, s)));
+    } else {
+      const StoreEpi<true>::Args ee = {a.dx, (int)a.rows, (int)a.c, vec_dx, lt, st};
+      CONV_TRY((gemm_launch<BF16, true, false, StoreEpi<true>>(gx, ee, p.dx.tile, 1, 1, s)));
+    }
     if (p.o_dwp >= 0) {
       float* part = f32_at(p.o_dwp);
       const int64_t stride = std::min(p.vp, a.classes) * p.cq;

@@ -59,6 +59,11 @@ __device__ __forceinline__ float g_at(const T* g, int64_t i) {
     return bf16_bits_to_f32(g[i]);
 }
 
+// The exponent of a finite v > 0, else 0 (infinities and NaN stay themselves).
+__device__ __forceinline__ int ilogb_f64(double v) {
+  return v > 0.0 && v < __builtin_inf() ? __builtin_amdgcn_frexp_exp(v) - 1 : 0;
+}
+
 // part[batch][kNormBlocks] = sums of squares in 64 bits (gridDim.x blocks fill them)
 template <typename T>
 __global__ __launch_bounds__(256) void norm_part_kernel(const T* g, int64_t count, double* part) {
@@ -110,15 +115,17 @@ __global__ __launch_bounds__(256) void start_kernel(const T* g, Layout l, const 
     }
   }
   __syncthreads();
-  // in 64 bits: the factor for a tiny G would leave fp32's range
+  // as inv_m 2^inv_k: the factor for a tiny G would leave fp32's range
   const double inv = (double)kSx / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)eps);
+  const int inv_k = ilogb_f64(inv);
+  const float inv_m = (float)__builtin_ldexp(inv, -inv_k);
   const int64_t xb = (int64_t)b * l.mp * l.np;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int u = (tid >> 4) + 16 * i, v = (tid & 15) * 4;
     float f[4], h[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = (float)((double)t[u][v + k] * inv);
+    for (int k = 0; k < 4; ++k) f[k] = __builtin_ldexpf(t[u][v + k] * inv_m, inv_k);
     const uint2 hv = {half2_bits(f[0], f[1]), half2_bits(f[2], f[3])};
     half4(hv, h);
     const int64_t o = xb + (int64_t)(m0 + u) * l.np + n0 + v;
@@ -373,11 +380,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 __device__ __forceinline__ f32x4 mfma_f16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-
-// The exponent of a finite v > 0, else 0 (infinities and NaN stay themselves).
-__device__ __forceinline__ int ilogb_f64(double v) {
-  return v > 0.0 && v < __builtin_inf() ? __builtin_amdgcn_frexp_exp(v) - 1 : 0;
 }
 
 // Four values of G from i on; vec: as one load.

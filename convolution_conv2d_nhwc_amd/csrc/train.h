@@ -67,7 +67,7 @@ struct HeadPlan {
   int64_t vp;      // classes per piece of the gradient, a multiple of 256
   int slots;       // (max, sum) pairs per row
   int stat_tile, ds_tile;
-  bool copy_x;
+  bool copy_x, pair;
   GemmShape dx, dw;
   int64_t o_stat, o_lab, o_x, o_w;                       // forward, copies
   int64_t o_lse, o_inv, o_delta, o_ds, o_dxp, o_dwp;     // gradient
