@@ -54,7 +54,8 @@ struct GemmArgs {
   int k;             // values of K; unless KS a multiple of 8
   int nq;            // tiles along q; symmetric products: tiles along either side
   int group;         // tile order: q tiles per group
-  int kt_per;        // K-tiles per split (gridDim.y splits)
+  int splits;        // of K, each
+  int kt_per;        // this many K-tiles
 };
 
 enum { BF16 = 0, FP16 = 1 };
@@ -265,14 +266,16 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   TileAt at;
   at.lane = lane;
-  at.split = blockIdx.y;
   at.batch = blockIdx.z;
 
   // Each XCD (block % 8 under round-robin dispatch) walks a contiguous
-  // run of tiles, `group` q tiles by all p tiles at a time, so that its L2
-  // holds the rows it re-reads.
+  // run of tiles, split after split, `group` q tiles by all p tiles at a time, so
+  // that its L2 holds the rows it re-reads.
   const int xcd = block & 7;
-  const int lin = xcd * (nwg >> 3) + min(xcd, nwg & 7) + (block >> 3);
+  int lin = xcd * (nwg >> 3) + min(xcd, nwg & 7) + (block >> 3);
+  const int tiles = nwg / g.splits;
+  at.split = lin / tiles;
+  lin -= at.split * tiles;
   int qt, pt;
   at.mirror = false;
   if constexpr (Epi::kSymmetric) {
@@ -283,7 +286,7 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
     qt = lin - pt * (pt + 1) / 2;
     at.mirror = qt != pt;
   } else {
-    const int npt = nwg / g.nq;
+    const int npt = tiles / g.nq;
     const int span = g.group * npt;
     const int grp = lin / span;
     const int first = grp * g.group;
@@ -310,7 +313,7 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
   const int step_a = sa.step(g.a_pitch), step_b = sb.step(g.b_pitch);
 
   // stages of SUB K-tiles: kt0 is this split's first K-tile
-  const int kt0 = blockIdx.y * g.kt_per;
+  const int kt0 = at.split * g.kt_per;
   const int kt_all = (g.k + kKV - 1) / kKV, kt_end = min(kt0 + g.kt_per, kt_all);
   const int nst = kt0 < kt_end ? (kt_end - kt0 + SUB - 1) / SUB : 0;  // 0: a split past the end, its sums are zeros
   const uint32_t lds_wave = (uint32_t)(uintptr_t)lds + wave * 1024;
@@ -441,12 +444,17 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
         else
           wait_loads<0>();
         wg_barrier();  // K-tile t + 1 is in LDS, K-tile t is in registers
-        slots(
-            [&](auto rc) {
-              if (decltype(inner)::value || t + NST < nst) dma_chunk(kt0 + t + NST, lds_wave + cur, inner, rc);
-              read_frag(lds + next, 0, rc, a0, b0);
-            },
-            a1, b1);
+        // a load keeps the CU's memory path busy for 64 cycles (four waves of 16), as
+        // long as four MFMAs
+        constexpr int LW = NMF / CH;
+        StaticFor<0, NMF>::run([&](auto kc) {
+          constexpr int m = decltype(kc)::value;
+          if constexpr (m % LW == 0)
+            if (decltype(inner)::value || t + NST < nst)
+              dma_chunk(kt0 + t + NST, lds_wave + cur, inner, std::integral_constant<int, m / LW>{});
+          if constexpr (m % W == 0 && m / W < NR) read_frag(lds + next, 0, std::integral_constant<int, m / W>{}, a0, b0);
+          mfma_range(kc, std::integral_constant<int, m + 1>{}, a1, b1);
+        });
         cur = next;
       };
       int t = 0;
@@ -586,6 +594,7 @@ inline void gemm_order(GemmArgs& g, int t, int splits) {
   // the 32 or 64 tiles that an XCD works on together make a block that is about
   // as wide as high: fewest rows fetched into its L2
   g.group = std::min(g.nq, t == 256 ? 6 : 8);
+  g.splits = splits;
   g.kt_per = cdiv(cdiv(g.k, kKV), splits);
 }
 
@@ -593,7 +602,7 @@ template <int DT, int T, bool DEEP, bool KSA, bool KSB, class Epi>
 hipError_t gemm_launch_t(GemmArgs g, const typename Epi::Args& e, int splits, int batch, hipStream_t s) {
   gemm_order(g, T, splits);
   const int tiles = (int)gemm_tiles(g.q, g.p, T, Epi::kSymmetric);
-  hipLaunchKernelGGL((gemm_kernel<DT, T, DEEP, KSA, KSB, Epi>), dim3(tiles, splits, batch), dim3(256), 0, s, g, e);
+  hipLaunchKernelGGL((gemm_kernel<DT, T, DEEP, KSA, KSB, Epi>), dim3(tiles * splits, 1, batch), dim3(256), 0, s, g, e);
   return hipGetLastError();
 }
 
