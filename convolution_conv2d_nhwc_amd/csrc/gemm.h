@@ -20,8 +20,8 @@
 // are short of workgroups, each wave owns the whole tile for a quarter of the K
 // values and the four sums meet in LDS at the end.
 //
-// Pipeline. K-tiles (T = 64: pairs) wait in an LDS ring: two stages for T = 256
-// (all that fits), two or four otherwise. One barrier a stage; operand reads and
+// Pipeline. K-tiles (T = 64: pairs) wait in an LDS ring: two stages and a half
+// for T = 256 (all that fits), two or four otherwise. One barrier a stage; operand reads and
 // loads go out over the first three quarters of the MFMAs before the ones that
 // need them, so that LDS latency and the barrier fall behind matrix work. Tried
 // and slower: K-tiles of 32 in a ring of four (rows of 64 bytes: twice the
@@ -234,7 +234,9 @@ struct SparseTerm {
   int p_base;           // the label of p = 0
   const float* delta;   // [K]
 };
-constexpr int kSparseCap = 2048;  // rows listed at a time
+constexpr int kSparseCap = 4096;  // rows listed at a time
+// a listed row: its number (the K of a product with a sparse term is below 2^22) and its p in the tile
+constexpr int kSparseRowBits = 22, kSparseRow = (1 << kSparseRowBits) - 1;
 
 __device__ __forceinline__ int64_t label_raw(const void* labels, int bytes, int64_t r) {
   return bytes == 8 ? static_cast<const int64_t*>(labels)[r] : static_cast<const int32_t*>(labels)[r];
@@ -247,10 +249,12 @@ struct Cut {
   static constexpr bool kSplitK = T == 64;       // waves share the tile, not K
   static constexpr int SUB = kSplitK ? 2 : 1;    // K-tiles of 64 per stage
   static constexpr int NST = T == 256 || !DEEP ? 2 : 4;
+  static constexpr bool kUnits = T == 256;         // a ring of operand tiles, not of stages
   static constexpr int NF = kSplitK ? 4 : T / 32;  // fragments of a wave along either side
   static constexpr int CH = SUB * 2 * (T / 32);    // loads per lane per stage
   static constexpr int TILE = T * kKB;             // bytes of one operand's K-tile
   static constexpr int STAGE = SUB * 2 * TILE;
+  static constexpr int LDS = kUnits ? 5 * TILE : NST * STAGE;
   static constexpr int FP = kSplitK ? 1 : NF;      // the epilogue's accumulators: [NF][FP]
 };
 
@@ -318,36 +322,41 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
   const int nst = kt0 < kt_end ? (kt_end - kt0 + SUB - 1) / SUB : 0;  // 0: a split past the end, its sums are zeros
   const uint32_t lds_wave = (uint32_t)(uintptr_t)lds + wave * 1024;
 
-  // load c of the stage whose first K-tile is kt, into LDS at `to`. Only the
+  // load c of the stage whose first K-tile is kt, into LDS at `to` (A) and to_b. Only the
   // last stage (not `inner`) can hold K's last tile, whose first load cuts off
   // the values past the end, and K-tiles past the split's end, loaded with
   // every lane past the buffer's.
   const int left = g.k - (kt_all - 1) * kKV;
-  auto dma_chunk = [&](int kt, uint32_t to, auto inner, auto cc) {
+  auto dma_chunk = [&](int kt, uint32_t to, uint32_t to_b, auto inner, auto cc) {
     constexpr int c = decltype(cc)::value, sub = c / (2 * NL), k = c % (2 * NL);
     constexpr bool in = decltype(inner)::value;
     const int at_kt = in ? kt + sub : min(kt + sub, kt_all - 1);
     const bool past = !in && SUB > 1 && kt + sub >= kt_end;
-    if constexpr (!in && k == 0) {
+    if constexpr (!in && (k == 0 || k == NL)) {
       if (left < kKV && kt + sub == kt_all - 1) {
-        sa.cut(left, tid);
-        sb.cut(left, tid);
+        if constexpr (k == 0)
+          sa.cut(left, tid);
+        else
+          sb.cut(left, tid);
       }
     }
     if constexpr (k < NL)
       load_lds<sub * 2 * TILE + k * 4096>(ra, to, past ? kPastEnd : sa.v[k], at_kt * step_a);
     else
-      load_lds<sub * 2 * TILE + TILE + (k - NL) * 4096>(rb, to, past ? kPastEnd : sb.v[k - NL], at_kt * step_b);
+      load_lds<sub * 2 * TILE + (k - NL) * 4096>(rb, to_b, past ? kPastEnd : sb.v[k - NL], at_kt * step_b);
   };
-  auto read_frag = [&](lds_ptr st, int s, auto rc, i32x4(&af)[F], i32x4(&bf)[F]) {
+  auto read_frag2 = [&](lds_ptr st, lds_ptr st_b, int s, auto rc, i32x4(&af)[F], i32x4(&bf)[F]) {
     constexpr int r = decltype(rc)::value;
     // in the order of use: a[0], all of b, the rest of a
     if constexpr (r == 0)
       af[0] = sa.read(st, s, 0);
     else if constexpr (r <= F)
-      bf[r - 1] = sb.read(st + TILE, s, r - 1);
+      bf[r - 1] = sb.read(st_b, s, r - 1);
     else
       af[r - F] = sa.read(st, s, r - F);
+  };
+  auto read_frag = [&](lds_ptr st, int s, auto rc, i32x4(&af)[F], i32x4(&bf)[F]) {
+    read_frag2(st, st + TILE, s, rc, af, bf);
   };
   auto read_all = [&](lds_ptr st, int s, i32x4(&af)[F], i32x4(&bf)[F]) {
     StaticFor<0, 2 * F>::run([&](auto rc) { read_frag(st, s, rc, af, bf); });
@@ -385,13 +394,30 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
     mfma_range(std::integral_constant<int, NR * W>{}, std::integral_constant<int, NMF>{}, af, bf);
   };
 
+  // the sparse term's first labels, loaded behind the product (as p of this tile, or -1)
+  constexpr int LR = Epi::kSparse ? 8 : 1;
+  int lab[LR];
+  auto load_labels = [&](int base) {
+    if constexpr (Epi::kSparse) {
+      const SparseTerm sp = Epi::sparse(e);
+      const int r1 = min(kt_end * kKV, g.k);
+#pragma unroll
+      for (int u = 0; u < LR; ++u) {
+        const int r = base + 64 * LR * wave + 64 * u + lane;
+        const int64_t l = r < r1 ? label_raw(sp.labels, sp.label_bytes, r) - sp.p_base - tp : -1;
+        lab[u] = l >= 0 && l < T && l + tp < g.p ? (int)l : -1;
+      }
+    }
+  };
+  load_labels(kt0 * kKV);
+
   i32x4 a0[F], b0[F], a1[F], b1[F];
   if (nst > 0) {
 #pragma unroll
     for (int k = 0; k < NST; ++k) {
       if (k < nst) {
         const int kt = kt0 + k * SUB;
-        StaticFor<0, CH>::run([&](auto cc) { dma_chunk(kt, lds_wave + k * STAGE, std::false_type{}, cc); });
+        StaticFor<0, CH>::run([&](auto cc) { dma_chunk(kt, lds_wave + k * STAGE, lds_wave + k * STAGE + TILE, std::false_type{}, cc); });
       }
     }
     if (nst >= NST)
@@ -414,7 +440,7 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
         wg_barrier();  // stage t + 1 is in LDS, stage t is in registers
         slots(
             [&](auto rc) {
-              if (decltype(inner)::value || t + NST < nst) dma_chunk(kt0 + (t + NST) * SUB, lds_wave + cur, inner, rc);
+              if (decltype(inner)::value || t + NST < nst) dma_chunk(kt0 + (t + NST) * SUB, lds_wave + cur, lds_wave + cur + TILE, inner, rc);
               read_frag(mine + next, half, rc, an, bn);
             },
             af, bf);
@@ -434,6 +460,47 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
         });
       }
       mfma_all(a0, b0);
+    } else if constexpr (C::kUnits) {
+      // Five units of one operand's K-tile: A(t) in unit 2 t mod 5, B(t) in the next. A(t + 2)
+      // is loaded in the first half of K-tile t (its unit held B(t - 1)), B(t + 2) in the second
+      // (its unit held A(t)): a load has at least a K-tile and a half, or a K-tile, to arrive.
+      auto after = [](int u, int n) { return u + n * TILE >= 5 * TILE ? u + n * TILE - 5 * TILE : u + n * TILE; };
+      int ua = 0, ub = TILE;
+      read_all(lds, 0, a0, b0);
+      constexpr int LW = NMF / NL;  // one load per so many MFMAs
+      auto body = [&](int t, auto inner) {
+        const int na = after(ua, 2), nb = after(ub, 2);
+        const uint32_t fa = lds_wave + after(ua, 4), fb = lds_wave + ua;
+        const bool more = decltype(inner)::value || t + 2 < nst;
+        StaticFor<0, NMF>::run([&](auto kc) {
+          constexpr int m = decltype(kc)::value;
+          if constexpr (m % LW == 0)
+            if (more) dma_chunk(kt0 + t + 2, fa, 0, inner, std::integral_constant<int, m / LW>{});
+          if constexpr (m % W == 0 && m / W < NR)
+            read_frag2(lds + ua, lds + ub, 1, std::integral_constant<int, m / W>{}, a1, b1);
+          mfma_range(kc, std::integral_constant<int, m + 1>{}, a0, b0);
+        });
+        if (more)
+          wait_loads<NL>();
+        else
+          wait_loads<0>();
+        wg_barrier();  // K-tile t + 1 is in LDS, K-tile t is in registers
+        StaticFor<0, NMF>::run([&](auto kc) {
+          constexpr int m = decltype(kc)::value;
+          if constexpr (m % LW == 0)
+            if (more) dma_chunk(kt0 + t + 2, 0, fb, inner, std::integral_constant<int, NL + m / LW>{});
+          if constexpr (m % W == 0 && m / W < NR)
+            read_frag2(lds + na, lds + nb, 0, std::integral_constant<int, m / W>{}, a0, b0);
+          mfma_range(kc, std::integral_constant<int, m + 1>{}, a1, b1);
+        });
+        ua = na;
+        ub = nb;
+      };
+      int t = 0;
+      for (; t + 3 < nst; ++t) body(t, std::true_type{});
+      for (; t + 1 < nst; ++t) body(t, std::false_type{});
+      slots([&](auto rc) { read_frag2(lds + ua, lds + ub, 1, rc, a1, b1); }, a0, b0);
+      mfma_all(a1, b1);
     } else {
       read_all(lds, 0, a0, b0);
       auto body = [&](int t, auto inner) {
@@ -451,7 +518,7 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
           constexpr int m = decltype(kc)::value;
           if constexpr (m % LW == 0)
             if (decltype(inner)::value || t + NST < nst)
-              dma_chunk(kt0 + t + NST, lds_wave + cur, inner, std::integral_constant<int, m / LW>{});
+              dma_chunk(kt0 + t + NST, lds_wave + cur, lds_wave + cur + TILE, inner, std::integral_constant<int, m / LW>{});
           if constexpr (m % W == 0 && m / W < NR) read_frag(lds + next, 0, std::integral_constant<int, m / W>{}, a0, b0);
           mfma_range(kc, std::integral_constant<int, m + 1>{}, a1, b1);
         });
@@ -474,14 +541,14 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
     const int r0 = kt0 * kKV, r1 = min(kt_end * kKV, g.k);
     int n = 0;
     wg_barrier();  // all waves have read the last stage
-    for (int base = r0; base < r1; base += 1024) {
-      // rows whose label lies in this tile's p, in order: wave w takes rows base + 256 w ..
-      int own[4], cnt = 0;
+    for (int base = r0; base < r1; base += 256 * LR) {
+      // rows whose label lies in this tile's p, in order: wave w takes 64 LR rows from
+      // base + 64 LR w on
+      if (base > r0) load_labels(base);
+      int own[LR], cnt = 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = base + 256 * wave + 64 * u + lane;
-        const int64_t l = r < r1 ? label_raw(sp.labels, sp.label_bytes, r) - sp.p_base - tp : -1;
-        const uint64_t m = __ballot(l >= 0 && l < T && l + tp < g.p);
+      for (int u = 0; u < LR; ++u) {
+        const uint64_t m = __ballot(lab[u] >= 0);
         own[u] = m >> lane & 1 ? cnt + __popcll(m & ((1ull << lane) - 1)) : -1;
         cnt += __popcll(m);
       }
@@ -494,26 +561,26 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
         all += counts[w];
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (own[u] >= 0) list[at0 + own[u]] = base + 256 * wave + 64 * u + lane;
+      for (int u = 0; u < LR; ++u)
+        if (own[u] >= 0) list[at0 + own[u]] = (base + 64 * LR * wave + 64 * u + lane) | lab[u] << kSparseRowBits;
       n += all;
       __syncthreads();
-      // room for another 1024: list on; else, or at the end, multiply what is listed
-      if (base + 1024 < r1 && n + 1024 <= kSparseCap) continue;
+      // room for another 256 LR: list on; else, or at the end, multiply what is listed
+      if (base + 256 * LR < r1 && n + 256 * LR <= kSparseCap) continue;
       for (int first = 0; first < n; first += SUB * kKV) {
         StaticFor<0, SUB * NL>::run([&](auto cc) {
           constexpr int sub = decltype(cc)::value / NL, c = decltype(cc)::value % NL;
           typedef Side<T, true, F> S;
           const int kk = first + sub * kKV + S::row_of(tid, c);
           const int col = at.tq + S::col_of(tid, c);
-          const uint32_t off = kk < n && col < g.q ? (uint32_t)list[kk] * (uint32_t)g.a_pitch + (uint32_t)col * 2 : kPastEnd;
+          const uint32_t off = kk < n && col < g.q ? (uint32_t)(list[kk] & kSparseRow) * (uint32_t)g.a_pitch + (uint32_t)col * 2 : kPastEnd;
           load_lds<sub * 2 * TILE + c * 4096>(ra, lds_wave, off, 0);
           *reinterpret_cast<i32x4*>(smem + sub * 2 * TILE + TILE + c * 4096 + tid * 16) = i32x4{0, 0, 0, 0};
         });
         __syncthreads();
         if (tid < SUB * kKV && first + tid < n) {
-          const int r = list[first + tid], kk = tid % kKV;
-          const int pl = (int)(label_raw(sp.labels, sp.label_bytes, r) - sp.p_base - tp);
+          const int r = list[first + tid] & kSparseRow, kk = tid % kKV;
+          const int pl = (int)((uint32_t)list[first + tid] >> kSparseRowBits);
           const int off = kk * 2 * T + ((pl >> 4) ^ Side<T, true, F>::swz(kk)) * 32 + (pl & 15) * 2;
           *reinterpret_cast<uint16_t*>(smem + (tid / kKV) * 2 * TILE + TILE + off) = f32_to_bf16_bits(sp.delta[r]);
         }
@@ -562,7 +629,7 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
 template <int DT, int T, bool DEEP, bool KSA, bool KSB, class Epi>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DEEP ? 1 : 2, DEEP ? 1 : 2))) void
 gemm_kernel(GemmArgs g, typename Epi::Args e) {
-  __shared__ __attribute__((aligned(16))) char smem[Cut<T, DEEP>::NST * Cut<T, DEEP>::STAGE];
+  __shared__ __attribute__((aligned(16))) char smem[Cut<T, DEEP>::LDS];
   gemm_tile_run<DT, T, DEEP, KSA, KSB, Epi>(g, e, smem, blockIdx.x, gridDim.x);
 }
 
@@ -571,7 +638,7 @@ gemm_kernel(GemmArgs g, typename Epi::Args e) {
 template <int DT, int T, class P0, class P1>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void
 gemm_pair_kernel(GemmArgs g0, typename P0::Epi::Args e0, int n0, GemmArgs g1, typename P1::Epi::Args e1) {
-  __shared__ __attribute__((aligned(16))) char smem[Cut<T, true>::NST * Cut<T, true>::STAGE];
+  __shared__ __attribute__((aligned(16))) char smem[Cut<T, true>::LDS];
   if ((int)blockIdx.x < n0)
     gemm_tile_run<DT, T, true, P0::KSA, P0::KSB, typename P0::Epi>(g0, e0, smem, blockIdx.x, n0);
   else

@@ -224,13 +224,15 @@ __device__ __forceinline__ void total_store(const FinishArgs& a, double t, int n
     cnt[wave] = n;
   }
   __syncthreads();
-  if (tid == 0) {
-    n = 0;
-    t = 0.0;
-    for (int i = 0; i < 16; ++i) {
-      n += cnt[i];
-      t += sum[i];
-    }
+  if (wave) return;
+  n = lane < 16 ? cnt[lane] : 0;
+  t = lane < 16 ? sum[lane] : 0.0;
+#pragma unroll
+  for (int k = 8; k >= 1; k >>= 1) {
+    n += __shfl_xor(n, k);
+    t += __shfl_xor(t, k);
+  }
+  if (lane == 0) {
     const double inv = 1.0 / (double)max(n, 1);
     a.total[0] = (float)(a.weights ? t : t * inv);
     if (a.inv) a.inv[0] = (float)inv;
@@ -533,28 +535,54 @@ __global__ __launch_bounds__(256) void part_sum_kernel(const float* part, int64_
   }
 }
 
-// Tile and splits of a product: whole reductions where the tiles fill the
-// chip, else splits of at least 8 K-tiles (512 values of K), as many as make
-// two rounds of 256 tiles or one of smaller ones.
+// Tile and splits of a product of k values of K: the least of an estimate in us,
+// rounds of workgroups times (K-tiles of 64 + what a tile costs besides), and
+// for a split the writing and adding of its sums at 3.5 TB/s. The figures are
+// measured ones: a K-tile of a 256 tile 1.65, of a 128 tile 0.8 alone on its CU
+// and 1.3 beside another, of a 64 tile 0.3 and 0.5. (1521 x 250 x 10007: dx in ten
+// splits of 128 tiles 20 us, dw in whole 128 tiles 25 us, in two splits 17 + 7;
+// 6400 x 1024 x 32768: dx in five splits of 256 tiles 390 us, unsplit 128 tiles
+// 690.)
 GemmShape shape_for(int64_t q, int64_t p, int64_t k) {
-  auto tiles = [&](int t) { return (int64_t)cdiv(q, t) * cdiv(p, t); };
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplit, k / 512));
-  if (tiles(256) >= 192) return {256, 1};
-  if (tiles(256) * most >= 192) return {256, (int)std::min<int64_t>(most, std::max<int64_t>(1, 512 / tiles(256)))};
-  if (tiles(128) * most >= 128) return {128, (int)std::min<int64_t>(most, std::max<int64_t>(1, 256 / tiles(128)))};
-  return {64, (int)std::min<int64_t>(most, std::max<int64_t>(1, 256 / tiles(64)))};
+  const int64_t kt = cdiv(k, kKV), most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplit, k / 512));
+  GemmShape best = {64, 1};
+  double least = 1e30;
+  for (int t = 64; t <= 256; t *= 2) {
+    const int64_t tiles = gemm_tiles(q, p, t, false);
+    for (int64_t s = 1; s <= most; ++s) {
+      const bool alone = t == 256 || tiles * s <= 256;
+      const double tile = t == 256 ? 1.65 : t == 128 ? (alone ? 0.8 : 1.3) : alone ? 0.3 : 0.5;
+      const double fixed = t == 256 ? 8.0 : t == 128 ? (alone ? 6.0 : 8.0) : alone ? 4.5 : 6.0;
+      double us = cdiv(tiles * s, alone ? 256 : 512) * (cdiv(kt, s) * tile + fixed);
+      if (s > 1) us += 3.0 + 8.0 * s * q * p / 3.5e6;
+      if (us < least) {
+        least = us;
+        best = {t, (int)s};
+      }
+    }
+  }
+  return best;
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 }  // namespace
 
+// Tile of the logits' products. Over few channels the epilogue is most of the
+// work, and two workgroups a CU hide one's behind the other's product (with
+// gradients, 128 / 256 tiles: 6400 x 128 x 30000 582 / 659 us, 4096 x 256 x
+// 16384 318 / 338, 4096 x 512 x 16384 457 / 453).
+static int logits_tile(int64_t classes, int64_t rows, int64_t c) {
+  const int t = gemm_tile(classes, rows, 1, false);
+  return t == 256 && c <= 256 ? 128 : t;
+}
+
 HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w) {
   HeadPlan p = {};
   const int64_t rows = d.rows, c = d.c, v = d.classes;
   p.cpad = up(c, 8);
   p.cq = up(c, 4);
-  p.stat_tile = gemm_tile(v, rows, 1, false);
+  p.stat_tile = logits_tile(v, rows, c);
   p.slots = p.stat_tile == 64 ? cdiv(v, 64) : 2 * cdiv(v, p.stat_tile);  // one per wave along the classes
   p.copy_x = copy_x;
   int64_t at = 0;
@@ -578,7 +606,7 @@ HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w)
     p.vp = up(cdiv(v, cdiv(v, most)), 256);
     const bool pieces = p.vp < v;
     const int64_t pv = std::min(p.vp, v);
-    p.ds_tile = gemm_tile(pv, rows, 1, false);
+    p.ds_tile = logits_tile(pv, rows, c);
     p.dx = shape_for(c, rows, pv);
     p.dw = shape_for(c, pv, rows);
     // short products in few tiles: both in one launch
