@@ -199,7 +199,59 @@ struct TileAt {
   int tq, wq;        // the tile's and the wave's first q
   int split, batch;
   int lane;
+  char* lds;         // kRelay bytes of the wave's own, free
   bool mirror;       // a symmetric product's tile off the diagonal
+};
+
+// The accumulators of one j, 16 p by 16 FQ q, as whole rows: eight consecutive q
+// a lane instead of four, 16 FQ / 8 lanes a row, through the wave's LDS (rows 16
+// bytes longer than their values: no two lanes of an access on a bank). Memory
+// then sees runs of 128 or 256 bytes; the accumulators' own layout gives runs of
+// 32 in sixteen rows an instruction (X of the 1024 x 4608 update, read and
+// written in its products' epilogue: 30 us a product that way, 22 this way).
+constexpr int kRelay = 16 * (128 + 4) * 4;
+template <int FQ>
+struct Rows {
+  static constexpr int kLanes = 2 * FQ;            // lanes per row
+  static constexpr int kPer = 64 / kLanes;         // rows per pass
+  static constexpr int kPasses = 16 / kPer;
+  int row, col;  // the lane's row in a pass, its first q in the wave's run
+  __device__ __forceinline__ explicit Rows(int lane) : row(lane / kLanes), col(lane % kLanes * 8) {}
+  // p of pass s of j, and q
+  __device__ __forceinline__ int p(const TileAt& at, int j, int s) const {
+    return at.p0 - (at.lane & 15) + 16 * j + row + s * kPer;
+  }
+  __device__ __forceinline__ int q(const TileAt& at) const { return at.wq + col; }
+  static __device__ __forceinline__ void fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // 32-bit values: put acc[0..FQ-1][j], then take row `row` of pass s
+  template <int FP>
+  static __device__ __forceinline__ void put(const TileAt& at, const f32x4 (&acc)[FQ][FP], int j) {
+    float* to = reinterpret_cast<float*>(at.lds) + (at.lane & 15) * (16 * FQ + 4) + 4 * (at.lane >> 4);
+    fence();
+#pragma unroll
+    for (int i = 0; i < FQ; ++i) *reinterpret_cast<f32x4*>(to + 16 * i) = acc[i][j];
+    fence();
+  }
+  __device__ __forceinline__ void take(const TileAt& at, int s, float (&f)[8]) const {
+    const f32x4* from =
+        reinterpret_cast<const f32x4*>(reinterpret_cast<float*>(at.lds) + (row + s * kPer) * (16 * FQ + 4) + col);
+    const f32x4 a = from[0], b = from[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[k] = a[k];
+      f[4 + k] = b[k];
+    }
+  }
+  // 16-bit values: put four of fragment i at the lane's p, take eight
+  static __device__ __forceinline__ void put16(const TileAt& at, int i, uint2 v) {
+    *reinterpret_cast<uint2*>(at.lds + (at.lane & 15) * (32 * FQ + 16) + 8 * (at.lane >> 4) + 32 * i) = v;
+  }
+  __device__ __forceinline__ uint4 take16(const TileAt& at, int s) const {
+    return *reinterpret_cast<const uint4*>(at.lds + (row + s * kPer) * (32 * FQ + 16) + 2 * col);
+  }
 };
 
 // What an epilogue loads before the product (here nothing).
@@ -249,7 +301,7 @@ struct Cut {
   static constexpr bool kSplitK = T == 64;       // waves share the tile, not K
   static constexpr int SUB = kSplitK ? 2 : 1;    // K-tiles of 64 per stage
   static constexpr int NST = T == 256 || !DEEP ? 2 : 4;
-  static constexpr bool kUnits = T == 256;         // a ring of operand tiles, not of stages
+  static constexpr bool kUnits = T == 256 || (T == 128 && !DEEP);  // a ring of operand tiles, not of stages
   static constexpr int NF = kSplitK ? 4 : T / 32;  // fragments of a wave along either side
   static constexpr int CH = SUB * 2 * (T / 32);    // loads per lane per stage
   static constexpr int TILE = T * kKB;             // bytes of one operand's K-tile
@@ -602,9 +654,10 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
   }
   guard_all();
 
+  wg_barrier();  // all waves have read the last stage
+  at.lds = smem + wave * kRelay;
   if constexpr (C::kSplitK) {
     // the waves' sums, in the waves' order: wave w ends with the 16 p of fragment w
-    wg_barrier();
     i32x4* const sums = reinterpret_cast<i32x4*>(smem);
     StaticFor<0, F>::run([&](auto ic) {
       StaticFor<0, F>::run([&](auto jc) {
@@ -620,6 +673,7 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
 #pragma unroll
       for (int w = 1; w < 4; ++w) sum[i][0] += __builtin_bit_cast(f32x4, sums[((w * F + wave) * F + i) * 64 + lane]);
     }
+    __syncthreads();
     Epi::template run<F, 1>(sum, at, e, pre);
   } else {
     Epi::template run<F, F>(acc, at, e, pre);

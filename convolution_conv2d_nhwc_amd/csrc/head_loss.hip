@@ -358,7 +358,8 @@ struct GradEpi {
       const Row in = pre.row(at, e, j);
       const float lse = in.lse, k = in.k;
       int d = in.d;
-      uint16_t* const row = e.ds + (int64_t)r * e.vp + at.q0;
+      const Rows<FQ> rows(at.lane);
+      rows.fence();
       if (ragged || __any(d >= 0 && d < 16 * FQ)) {
         d -= at.q0 - at.wq;
         StaticFor<0, FQ>::run([&](auto ic) {
@@ -373,8 +374,7 @@ struct GradEpi {
             if (at.q0 + 16 * i + z >= e.nv) g[z] = 0.0f;
             if (hit) e.delta[r] = g[z] - bf16_bits_to_f32(f32_to_bf16_bits(g[z]));
           }
-          const uint2 v = {bf16x2_bits(g[0], g[1]), bf16x2_bits(g[2], g[3])};
-          if (r < e.rows) *reinterpret_cast<uint2*>(row + 16 * i) = v;
+          rows.put16(at, i, uint2{bf16x2_bits(g[0], g[1]), bf16x2_bits(g[2], g[3])});
         });
       } else {
         StaticFor<0, FQ>::run([&](auto ic) {
@@ -382,9 +382,14 @@ struct GradEpi {
           float g[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) g[z] = k * exp2_f32(__builtin_fmaf(acc[i][j][z], kLog2e, -lse));
-          const uint2 v = {bf16x2_bits(g[0], g[1]), bf16x2_bits(g[2], g[3])};
-          if (r < e.rows) *reinterpret_cast<uint2*>(row + 16 * i) = v;
+          rows.put16(at, i, uint2{bf16x2_bits(g[0], g[1]), bf16x2_bits(g[2], g[3])});
         });
+      }
+      rows.fence();
+#pragma unroll
+      for (int s = 0; s < rows.kPasses; ++s) {
+        const int p = rows.p(at, j, s);
+        if (p < e.rows) *reinterpret_cast<uint4*>(e.ds + (int64_t)p * e.vp + rows.q(at)) = rows.take16(at, s);
       }
     });
   }
@@ -428,7 +433,7 @@ struct StoreEpi {
   struct Args {
     uint16_t* out;
     int rows, c;
-    int vec;  // c % 4 == 0 and out 8-byte aligned
+    int vec;  // c % 8 == 0 and out 16-byte aligned
     LabelTerm lt;
     SparseTerm st;
   };
@@ -440,24 +445,36 @@ struct StoreEpi {
     StaticFor<0, FP>::run([&](auto jc) {
       constexpr int j = decltype(jc)::value;
       const int r = at.p0 + 16 * j;
-      if (r >= e.rows) return;
       LabelRow l = {};
-      if constexpr (DX) l = label_row(e.lt, r);
+      if constexpr (DX)
+        if (r < e.rows) l = label_row(e.lt, r);
+      const Rows<FQ> rows(at.lane);
+      rows.fence();
       StaticFor<0, FQ>::run([&](auto ic) {
         constexpr int i = decltype(ic)::value;
         const int q = at.q0 + 16 * i;
-        if (q >= e.c) return;
-        uint16_t* o = e.out + (int64_t)r * e.c + q;
         f32x4 v = acc[i][j];
-        if constexpr (DX) v = label_add(v, l, q);
-        if (e.vec) {
-          *reinterpret_cast<uint2*>(o) = uint2{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
-        } else {
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            if (q + z < e.c) o[z] = f32_to_bf16_bits(v[z]);
-        }
+        if constexpr (DX)
+          if (q < e.c) v = label_add(v, l, q);
+        rows.put16(at, i, uint2{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])});
       });
+      rows.fence();
+#pragma unroll
+      for (int s = 0; s < rows.kPasses; ++s) {
+        const int p = rows.p(at, j, s), q = rows.q(at);
+        if (p >= e.rows || q >= e.c) continue;
+        const uint4 v = rows.take16(at, s);
+        uint16_t* o = e.out + (int64_t)p * e.c + q;
+        if (e.vec) {
+          *reinterpret_cast<uint4*>(o) = v;
+        } else {
+          uint16_t u[8];
+          __builtin_memcpy(u, &v, 16);
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            if (q + z < e.c) o[z] = u[z];
+        }
+      }
     });
   }
 };
@@ -697,8 +714,10 @@ hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s) {
 
   uint16_t* ds = reinterpret_cast<uint16_t*>(at(p.o_ds));
   float* delta = f32_at(p.o_delta);
-  const int vec_dx = a.c % 4 == 0 && ((uintptr_t)a.dx & 7) == 0;
-  const int vec_dw = a.c % 4 == 0 && ((uintptr_t)a.dw & 7) == 0;
+  const int vec_dx = a.c % 8 == 0 && ((uintptr_t)a.dx & 15) == 0;
+  const int vec_dw = a.c % 8 == 0 && ((uintptr_t)a.dw & 15) == 0;
+  const int sum_vec_dx = a.c % 4 == 0 && ((uintptr_t)a.dx & 7) == 0;
+  const int sum_vec_dw = a.c % 4 == 0 && ((uintptr_t)a.dw & 7) == 0;
   const int64_t dx_stride = a.rows * p.cq;
   for (int64_t v0 = 0; v0 < a.classes; v0 += p.vp) {
     const int64_t nv = std::min(p.vp, a.classes - v0);
@@ -748,14 +767,14 @@ hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s) {
       const int64_t stride = std::min(p.vp, a.classes) * p.cq;
       const PartEpi<false>::Args pe = {part, stride, (int)nv, (int)p.cq, 0, lt, st};
       CONV_TRY((gemm_launch<BF16, true, true, PartEpi<false>>(gw, pe, p.dw.tile, p.dw.splits, 1, s)));
-      CONV_TRY(launch_part_sum(part, stride, p.dw.splits, nv, a.c, p.cq, dw, vec_dw, s));
+      CONV_TRY(launch_part_sum(part, stride, p.dw.splits, nv, a.c, p.cq, dw, sum_vec_dw, s));
     } else {
       const StoreEpi<false>::Args ee = {dw, (int)nv, (int)a.c, vec_dw, lt, st};
       CONV_TRY((gemm_launch<BF16, true, true, StoreEpi<false>>(gw, ee, p.dw.tile, 1, 1, s)));
     }
   }
   if (p.o_dxp >= 0)
-    CONV_TRY(launch_part_sum(f32_at(p.o_dxp), dx_stride, p.dx.splits, a.rows, a.c, p.cq, a.dx, vec_dx, s));
+    CONV_TRY(launch_part_sum(f32_at(p.o_dxp), dx_stride, p.dx.splits, a.rows, a.c, p.cq, a.dx, sum_vec_dx, s));
   return hipSuccess;
 }
 

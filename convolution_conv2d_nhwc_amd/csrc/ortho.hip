@@ -104,15 +104,26 @@ __global__ __launch_bounds__(256) void start_kernel(const T* g, Layout l, const 
   for (int k = 32; k >= 1; k >>= 1) s += __shfl_xor(s, k);
   if ((tid & 63) == 0) red[tid >> 6] = s;
   const T* gb = g + (int64_t)b * l.m * l.n;
-  // t[i][j] = X[m0 + i][n0 + j], read along G's rows either way round
+  // t[i][j] = X[m0 + i][n0 + j], read along G's rows either way round; all loads
+  // before the first store (one latency)
+  const int u0 = tid >> 6, v = tid & 63;
+  float r[16];
+  if (l.tall) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int u = (tid >> 6) + 4 * i, v = tid & 63;
-    if (l.tall) {
-      t[v][u] = n0 + u < l.n && m0 + v < l.m ? g_at(gb, (int64_t)(n0 + u) * l.m + m0 + v) : 0.0f;
-    } else {
-      t[u][v] = m0 + u < l.m && n0 + v < l.n ? g_at(gb, (int64_t)(m0 + u) * l.n + n0 + v) : 0.0f;
+    for (int i = 0; i < 16; ++i) {
+      const int u = u0 + 4 * i;
+      r[i] = n0 + u < l.n && m0 + v < l.m ? g_at(gb, (int64_t)(n0 + u) * l.m + m0 + v) : 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[v][u0 + 4 * i] = r[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int u = u0 + 4 * i;
+      r[i] = m0 + u < l.m && n0 + v < l.n ? g_at(gb, (int64_t)(m0 + u) * l.n + n0 + v) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[u0 + 4 * i][v] = r[i];
   }
   __syncthreads();
   // as inv_m 2^inv_k: the factor for a tiny G would leave fp32's range
@@ -275,6 +286,17 @@ struct PolyEpi {
   }
 };
 
+__device__ __forceinline__ void half8(uint4 v, float (&f)[8]) {
+  float a[4], b[4];
+  half4(uint2{v.x, v.y}, a);
+  half4(uint2{v.z, v.w}, b);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[k] = a[k];
+    f[4 + k] = b[k];
+  }
+}
+
 // X <- E_p X_p + R X, from hi (which the product reads) to the next hi, lo in
 // place, or to the result of the last step.
 struct StepEpi {
@@ -285,24 +307,25 @@ struct StepEpi {
     _Float16* next;
     _Float16* lo;
     uint16_t* out;    // last step: [m][n], or [n][m] when tall; else null
-    int out_vec;      // rows of out are whole 8-byte vectors
+    int out_vec;      // rows of out are whole 16-byte vectors
     Layout l;
   };
+  // hi, lo and E of the 16 p of one j, as Rows has them
   template <int FQ>
   struct Row {
-    uint2 h[FQ], g[FQ];
-    float ep;
+    uint4 h[Rows<FQ>::kPasses], g[Rows<FQ>::kPasses];
+    float ep[Rows<FQ>::kPasses];
     __device__ __forceinline__ void load(const TileAt& at, const Args& e, int j) {
-      const int p = at.p0 + 16 * j;
-      if (p >= e.l.mp) return;
-      const int64_t b = (int64_t)at.batch * e.l.mp;
-      ep = e.e[b + p];
+      const Rows<FQ> rows(at.lane);
+      const int q = rows.q(at);
 #pragma unroll
-      for (int i = 0; i < FQ; ++i) {
-        const int64_t o = (b + p) * e.l.np + at.q0 + 16 * i;
-        if (at.q0 + 16 * i < e.l.np) {
-          h[i] = *reinterpret_cast<const uint2*>(e.hi + o);
-          g[i] = *reinterpret_cast<const uint2*>(e.lo + o);
+      for (int s = 0; s < rows.kPasses; ++s) {
+        const int p = rows.p(at, j, s);
+        if (p < e.l.mp && q < e.l.np) {
+          const int64_t b = (int64_t)at.batch * e.l.mp + p;
+          ep[s] = e.e[b];
+          h[s] = *reinterpret_cast<const uint4*>(e.hi + b * e.l.np + q);
+          g[s] = *reinterpret_cast<const uint4*>(e.lo + b * e.l.np + q);
         }
       }
     }
@@ -313,41 +336,46 @@ struct StepEpi {
   static __device__ __forceinline__ void run(f32x4 (&acc)[FQ][FP], const TileAt& at, const Args& e,
                                              Pre<FQ, FP>& pre) {
     const Layout l = e.l;
-    const int64_t xb = (int64_t)at.batch * l.mp * l.np;
     uint16_t* out = e.out ? e.out + (int64_t)at.batch * l.m * l.n : nullptr;
+    const Rows<FQ> rows(at.lane);
+    const int q = rows.q(at);
     StaticFor<0, FP>::run([&](auto jc) {
       constexpr int j = decltype(jc)::value;
       const Row<FQ> row = pre.template next<j>(at, e);
-      const int p = at.p0 + 16 * j;
-      if (p >= l.mp) return;
-      StaticFor<0, FQ>::run([&](auto ic) {
-        constexpr int i = decltype(ic)::value;
-        const int q = at.q0 + 16 * i;
-        if (q >= l.np) return;
-        const int64_t o = xb + (int64_t)p * l.np + q;
-        float h[4], g[4], f[4];
-        half4(row.h[i], h);
-        half4(row.g[i], g);
+      rows.put(at, acc, j);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) f[z] = row.ep * (h[z] + g[z]) + acc[i][j][z] * (1.0f / kSr);
+      for (int s = 0; s < rows.kPasses; ++s) {
+        const int p = rows.p(at, j, s);
+        float f[8], h[8], g[8];
+        rows.take(at, s, f);
+        if (p >= l.mp || q >= l.np) continue;
+        half8(row.h[s], h);
+        half8(row.g[s], g);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) f[z] = row.ep[s] * (h[z] + g[z]) + f[z] * (1.0f / kSr);
         if (!out) {
-          const uint2 hv = {half2_bits(f[0], f[1]), half2_bits(f[2], f[3])};
-          half4(hv, h);
-          *reinterpret_cast<uint2*>(e.next + o) = hv;
-          *reinterpret_cast<uint2*>(e.lo + o) =
-              uint2{half2_bits(f[0] - h[0], f[1] - h[1]), half2_bits(f[2] - h[2], f[3] - h[3])};
-        } else {
+          const int64_t o = ((int64_t)at.batch * l.mp + p) * l.np + q;
+          const uint4 hv = {half2_bits(f[0], f[1]), half2_bits(f[2], f[3]), half2_bits(f[4], f[5]),
+                            half2_bits(f[6], f[7])};
+          half8(hv, h);
+          *reinterpret_cast<uint4*>(e.next + o) = hv;
+          *reinterpret_cast<uint4*>(e.lo + o) =
+              uint4{half2_bits(f[0] - h[0], f[1] - h[1]), half2_bits(f[2] - h[2], f[3] - h[3]),
+                    half2_bits(f[4] - h[4], f[5] - h[5]), half2_bits(f[6] - h[6], f[7] - h[7])};
+        } else if (p < l.m) {
           const float k = 1.0f / kSx;
-          const uint2 v = {bf16x2_bits(f[0] * k, f[1] * k), bf16x2_bits(f[2] * k, f[3] * k)};
-          if (l.tall) {
-            const uint2 t = quad_transpose(v, at.lane);
-            const int row = q + (at.lane & 3), col = p & ~3;
-            if (row < l.n) put4(out + (int64_t)row * l.m + col, t, l.m - col, e.out_vec);
-          } else if (p < l.m) {
-            put4(out + (int64_t)p * l.n + q, v, l.n - q, e.out_vec);
+          if (!l.tall && e.out_vec) {
+            if (q < l.n)
+              *reinterpret_cast<uint4*>(out + (int64_t)p * l.n + q) =
+                  uint4{bf16x2_bits(f[0] * k, f[1] * k), bf16x2_bits(f[2] * k, f[3] * k),
+                        bf16x2_bits(f[4] * k, f[5] * k), bf16x2_bits(f[6] * k, f[7] * k)};
+          } else {
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              if (q + z < l.n) out[l.tall ? (int64_t)(q + z) * l.m + p : (int64_t)p * l.n + q + z] = f32_to_bf16_bits(f[z] * k);
           }
         }
-      });
+      }
     });
   }
 };
@@ -675,6 +703,7 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   const Layout l = layout_of(a.rows, a.cols);
   const int out_row = l.tall ? l.m : l.n;
   const int out_vec = out_row % 4 == 0 && ((uintptr_t)a.out & 7) == 0;
+  const int out_vec8 = l.n % 8 == 0 && ((uintptr_t)a.out & 15) == 0;
   const OrthoWs w = ortho_layout(a.batch, l);
   if (!w.bytes) {
     if (a.g_f32)
@@ -717,7 +746,7 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
     g.a_pitch = l.np * 2;
     g.a_batch = (int64_t)l.mp * l.np * 2;
     g.q = l.np;
-    const StepEpi::Args sa = {e, hi, next, lo, last ? a.out : nullptr, out_vec, l};
+    const StepEpi::Args sa = {e, hi, next, lo, last ? a.out : nullptr, out_vec8, l};
     err = gemm_launch<FP16, true, false, StepEpi>(g, sa, step_tile, 1, a.batch, s);
     if (err != hipSuccess) return err;
   }
