@@ -70,8 +70,17 @@ __device__ __forceinline__ void mfma_acc(f32x4& c, const i32x4& a, const i32x4& 
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b) : "memory");
 }
 
-// Wait states between a VALU access of an accumulator and an MFMA on it.
-__device__ __forceinline__ void acc_guard(f32x4& c) { asm volatile("s_nop 4" : "+a"(c)); }
+// The accumulators as one point in the program: between it and an MFMA, or an
+// MFMA and it, go the wait states that the hardware asks for (a VALU write
+// before an MFMA's read: at most 4; an MFMA's result before a VALU or store
+// reads it: at most 18).
+template <int FQ, int FP>
+__device__ __forceinline__ void acc_pin(f32x4 (&c)[FQ][FP]) {
+#pragma unroll
+  for (int i = 0; i < FQ; ++i)
+#pragma unroll
+    for (int j = 0; j < FP; ++j) asm volatile("" : "+a"(c[i][j]));
+}
 
 // Operands that the compiler may just have moved: a VALU write needs two wait
 // states before an MFMA reads it, and it does not know the ones above for MFMAs.
@@ -419,12 +428,8 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
   for (int i = 0; i < F; ++i)
 #pragma unroll
     for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  auto guard_all = [&]() {
-    StaticFor<0, F>::run([&](auto ic) {
-      StaticFor<0, F>::run([&](auto jc) { acc_guard(acc[decltype(ic)::value][decltype(jc)::value]); });
-    });
-  };
-  guard_all();
+  acc_pin(acc);
+  asm volatile("s_nop 4");
   auto mfma_range = [&](auto bc, auto ec, const i32x4(&af)[F], const i32x4(&bf)[F]) {
     StaticFor<decltype(bc)::value, decltype(ec)::value>::run([&](auto kc) {
       constexpr int k = decltype(kc)::value;
@@ -652,7 +657,8 @@ __device__ __forceinline__ void gemm_tile_run(const GemmArgs& g, const typename 
       n = 0;
     }
   }
-  guard_all();
+  asm volatile("s_nop 15\n\ts_nop 3");
+  acc_pin(acc);
 
   wg_barrier();  // all waves have read the last stage
   at.lds = smem + wave * kRelay;
