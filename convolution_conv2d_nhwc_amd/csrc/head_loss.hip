@@ -21,6 +21,11 @@
 // tile from the first pass, rounds twice to bf16 and stores rows * classes
 // values all the same.
 //
+// What bounds it: the matrix cores at large sizes (6400 x 1024 x 65536, all
+// gradients: 3.15 ms, of which logits 0.78, logits again with g 0.92, dx 0.76, dw
+// 0.66 ms), the fixed cost of eight launches at small ones (1521 x 250 x 10007:
+// 92 us as a call, 99 us of kernels under a profiler).
+//
 // Precision. Rounding g to bf16 would cost as much as the rounding of the
 // results, nearly all of it from the one large entry of a row, its label's.
 // What that rounding left out, delta[r], is kept in fp32 and put back: in dx as

@@ -24,7 +24,8 @@
 // between lanes), so a step costs m m n + m m m + 2 m m n operations. All
 // sides are padded to multiples of 64 with zeros, which the iteration keeps
 // zero. What bounds it: the matrix cores at large sizes; at small ones the
-// 3 steps + 2 launches.
+// 3 steps + 2 launches. 1024 x 4608 in five steps: 255 us, a step 18 (A) + 9 (Q)
+// + 22 (Q X), and 14 before the first; six of 250 x 1000: 122 us.
 #include "gemm.h"
 #include "train.h"
 

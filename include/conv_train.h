@@ -118,7 +118,8 @@ conv_status conv_head_loss(const conv_head_desc* d, const void* x, const void* w
  *   dx[r]   = sum_v g[r][v] w[v],   dw[v] = sum_r g[r][v] x[r]
  *   dx : device [rows][c], dw : device [classes][c], bf16
  * g is rounded to bf16 once for the two products (half a bf16 step of each
- * term; the sums run in fp32 and are rounded to bf16 once). */
+ * term), but what that leaves out of a row's label entry is kept in fp32 and
+ * added back; the sums run in fp32 and are rounded to bf16 once. */
 conv_status conv_head_loss_grad(const conv_head_desc* d, const void* x, const void* w, const void* labels,
                                 const float* weights, float* loss, float* total, void* dx, void* dw, void* ws,
                                 int64_t ws_bytes, void* stream);
@@ -140,8 +141,9 @@ int64_t conv_orthogonalize_ws_bytes(const conv_ortho_desc* d);
 
 /*   g   : device [batch][rows][cols] of dtype
  *   out : device [batch][rows][cols] bf16 (one RNE rounding)
- * The products run on fp16 matrix instructions with fp32 sums; X is held as a
- * pair of fp16 (22 bits), the diagonals of A and of the polynomial in fp32,
+ * Matrices whose shorter side is at most 64 and longer at most 1024 need no
+ * scratch. The products run on fp16 matrix instructions with fp32 sums; X is
+ * held as a pair of fp16 (22 bits; fp32 without scratch), the diagonals of A and of the polynomial in fp32,
  * so that the result is off by less than half of a bf16 step for
  * coefficients that keep the singular values within [0, 2]. Values are
  * scaled by powers of two to stay in fp16's range; coefficients under which
