@@ -754,9 +754,9 @@ hipError_t launch_vec(const NormArgs& a, bool grad, hipStream_t s) {
     case 1: return launch_whole<T, VEC, SAME, 1>(a, grad, s);
     case 2: return launch_whole<T, VEC, SAME, 2>(a, grad, s);
     case 4: return launch_whole<T, VEC, SAME, 4>(a, grad, s);
-    case 8:
-      return a.p.threads == kThreads ? launch_whole<T, VEC, SAME, 8>(a, grad, s)
-                                     : launch_whole<T, VEC, SAME, 8, 2 * kThreads>(a, grad, s);
+    case kSteps:
+      return a.p.threads == kThreads ? launch_whole<T, VEC, SAME, kSteps>(a, grad, s)
+                                     : launch_whole<T, VEC, SAME, kSteps, 2 * kThreads>(a, grad, s);
   }
   const dim3 grid(a.p.chunks, a.p.ctiles, a.n);
   const dim3 more(a.p.chunks + (a.dgamma || a.dbeta), a.p.ctiles, a.n);
@@ -846,15 +846,18 @@ NormPlan norm_plan(const conv_norm_desc& d, bool grad, int align) {
     // 42 / 37; 32 bytes: 28, 60)
     for (int run = 128; run >= 32; run /= 2) {
       if (run < (grad ? 128 : 64) && d.n * hw * c * esz > 4 << 20) break;
-      int64_t need = cut(run);
+      const int64_t need = cut(run);
       if (need > 2 * kSteps) continue;
       p.threads = kThreads;
       if (need > kSteps) {
+        // 1024 lanes take at least two pixels a step for each that 512 took, so kSteps
+        // vectors suffice; their kernel has that many also where fewer would do
         p.threads *= 2;
         p.ppi = p.threads / (p.ct / p.vec);
-        need = (hw + p.ppi - 1) / p.ppi;
+        p.r = kSteps;
+      } else {
+        for (p.r = 1; p.r < need;) p.r *= 2;
       }
-      for (p.r = 1; p.r < need;) p.r *= 2;
       if (d.n * p.ctiles >= 256) break;
     }
     if (p.r) return p;

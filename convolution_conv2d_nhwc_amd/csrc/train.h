@@ -25,7 +25,7 @@ struct NormPlan {
   int ctiles;  // channel tiles
   int ppi;     // pixels a workgroup covers per step
   int r;       // one launch: vectors a lane keeps in registers; 0: streamed
-  int threads; // lanes of a workgroup
+  int threads; // lanes of a workgroup: 512, or 1024 for one launch with the most vectors a lane
   int chunks;  // pixel chunks per image (one launch: 1)
   int cpix;    // pixels per chunk, whole blocks
 };

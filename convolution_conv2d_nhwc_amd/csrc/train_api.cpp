@@ -2,6 +2,7 @@
 // (include/conv_train.h): argument checks on the host, then the launchers.
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 
 #include "train.h"
 
@@ -201,6 +202,19 @@ int64_t conv_group_norm_ws_bytes(const conv_norm_desc* d, int32_t grad) {
   if (st != CONV_OK) return st;
   const int64_t b = norm_ws(*d, grad != 0);
   return b >= kMaxBytes ? (int64_t)CONV_E_UNSUPPORTED : b;
+}
+
+conv_status conv_group_norm_describe(const conv_norm_desc* d, int32_t grad, int32_t align, char* buf, int32_t len) {
+  if (!d || !buf || len <= 0) return CONV_E_NULL;
+  const conv_status st = norm_check(d);
+  if (st != CONV_OK) return st;
+  const NormPlan p = norm_plan(*d, grad != 0, align_of(reinterpret_cast<const void*>((uintptr_t)align)));
+  std::snprintf(buf, len,
+                "group_norm%s %s dtype=%s vec=%d ct=%d gpt=%d tpg=%d ctiles=%d ppi=%d r=%d threads=%d chunks=%d "
+                "cpix=%d",
+                grad ? "_grad" : "", p.r ? "whole" : "streamed", d->dtype == CONV_F32 ? "f32" : "bf16", p.vec, p.ct,
+                p.gpt, p.tpg, p.ctiles, p.ppi, p.r, p.threads, p.chunks, p.cpix);
+  return CONV_OK;
 }
 
 conv_status conv_group_norm(const conv_norm_desc* d, const void* x, const float* gamma, const float* beta, void* y,

@@ -51,6 +51,8 @@ def _L():
         ND = ctypes.POINTER(_NormDesc)
         L.conv_group_norm_ws_bytes.argtypes = [ND, I32]
         L.conv_group_norm_ws_bytes.restype = I64
+        L.conv_group_norm_describe.argtypes = [ND, I32, I32, ctypes.c_char_p, I32]
+        L.conv_group_norm_describe.restype = ctypes.c_int
         L.conv_group_norm.argtypes = [ND, P, P, P, P, P, P, I64, P]
         L.conv_group_norm.restype = ctypes.c_int
         L.conv_group_norm_grad.argtypes = [ND] + [P] * 9 + [I64, P]

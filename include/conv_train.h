@@ -51,6 +51,10 @@ typedef struct conv_norm_desc {
 /* Scratch of conv_group_norm (grad = 0) or conv_group_norm_grad (grad = 1). */
 int64_t conv_group_norm_ws_bytes(const conv_norm_desc* d, int32_t grad);
 
+/* Human-readable description of the launch that x, y, dy and dx of the given
+ * common byte alignment (1 .. 16) take, as conv_describe writes it for a layer. */
+conv_status conv_group_norm_describe(const conv_norm_desc* d, int32_t grad, int32_t align, char* buf, int32_t len);
+
 /*   x           : device [n][h][w] pixels x_pixel_stride elements apart
  *   gamma, beta : device float[c], or NULL for 1 and 0
  *   y           : device [n][h][w][c] of dtype

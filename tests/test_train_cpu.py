@@ -205,3 +205,56 @@ def test_ws_bytes_from_python_raise_named_errors():
         train.orthogonalize_ws_bytes(1, 40000, 10)
     assert e.value.name == "CONV_E_UNSUPPORTED"
     assert train.head_loss_ws_bytes(100, 64, 1000, grad=True) > train.head_loss_ws_bytes(100, 64, 1000) > 0
+
+
+def described(call, *args):
+    """The key=value fields of a describe entry point's text."""
+    buf = ctypes.create_string_buffer(256)
+    assert call(*args, buf, 256) == 0
+    return {k: int(v) if v.isdigit() else v for k, v in (f.split("=") for f in buf.value.decode().split() if "=" in f)}
+
+
+# n, h, w, c, groups, dtype: maps whose tile needs 3 or 4 vectors of 1024 lanes but over 8 of 512
+ODD_LANES = [(1, 18, 25, 72, 1, 1), (4, 15, 30, 576, 8, 1), (1, 14, 15, 76, 4, 1), (1, 11, 14, 104, 1, 0),
+             (16, 17, 17, 448, 32, 0), (1, 3, 3, 301, 1, 0)]
+
+
+def norm_plan_problem(shape, dtype, align, grad):
+    n, h, w, c, groups = shape
+    p = described(train._L().conv_group_norm_describe, norm_desc(n=n, h=h, w=w, c=c, groups=groups, dtype=dtype), grad, align)
+    # the kernels are built for 512 lanes, and for 1024 with 8 vectors each
+    if p["threads"] not in (512, 1024) or (p["threads"] == 1024 and p["r"] != 8):
+        return "lanes"
+    if p["r"] not in (0, 1, 2, 4, 8) or p["ct"] % p["vec"] or p["ct"] > 512:
+        return "variant"
+    if p["ppi"] < 1 or p["ppi"] * (p["ct"] // p["vec"]) > p["threads"]:
+        return "more lanes than launched"
+    cg = c // groups
+    covered = p["ctiles"] // p["tpg"] * p["gpt"] >= groups and (p["gpt"] * cg == p["ct"] if p["tpg"] == 1 else p["tpg"] * p["ct"] >= cg)
+    if not covered or c % p["vec"]:
+        return "channels left over"
+    if p["r"] and p["r"] * p["ppi"] < h * w:
+        return "pixels left over"
+    if p["chunks"] * p["cpix"] < h * w or (p["chunks"] - 1) * p["cpix"] >= h * w:
+        return "chunks"
+    return None
+
+
+@pytest.mark.parametrize("grad", [0, 1])
+@pytest.mark.parametrize("shape", ODD_LANES, ids=lambda s: "x".join(map(str, s)))
+def test_group_norm_plan_of_1024_lanes(shape, grad):
+    for align in (2, 4, 8, 16):
+        assert norm_plan_problem(shape[:5], shape[5], align, grad) is None
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_group_norm_plan_covers_the_map(dtype):
+    """Every plan's lanes exist, and reach every channel and pixel."""
+    for cg in list(range(1, 130)) + [144, 171, 192, 256, 301, 341, 400, 511, 512, 513, 640, 1030]:
+        for groups in (1, 2, 3, 8, 32):
+            if cg * groups > 4096:
+                continue
+            for hw in list(range(1, 70, 3)) + [100, 150, 289, 450, 777, 1600, 6400, 22500]:
+                for n, grad, align in ((1, 0, 16), (4, 1, 16), (1, 1, 2)):
+                    shape = (n, 1, hw, cg * groups, groups)
+                    assert norm_plan_problem(shape, dtype, align, grad) is None, (shape, grad, align)

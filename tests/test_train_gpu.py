@@ -620,3 +620,18 @@ def test_fitting_a_head_lowers_its_loss():
     losses = fit.run(steps=60, classes=50, quiet=True)
     assert abs(losses[0] - 3.912) < 0.5
     assert losses[-1] < 0.5 * losses[0], losses
+
+
+# ------------------------------------------------------------ cases of one variant each --
+
+@pytest.mark.parametrize("shape", [(1, 18, 25, 72, 1, "bf16"), (4, 15, 30, 576, 8, "bf16"), (1, 14, 15, 76, 4, "bf16"),
+                                   (1, 11, 14, 104, 1, "f32"), (16, 17, 17, 448, 32, "f32"), (1, 3, 3, 301, 1, "f32"),
+                                   (1, 3, 3, 301, 1, "bf16"), (1, 45, 10, 9, 3, "bf16")],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_group_norm_of_1024_lanes_with_few_vectors(shape):
+    """Maps of over 8 vectors for each of 512 lanes, but 3 or 4 for each of 1024."""
+    n, h, w, c, groups, dtype = shape
+    g = gen(c)
+    x, dy = (torch.randn((n, h, w, c), generator=g).to(DT[dtype]) for _ in range(2))
+    gamma, beta = 1 + 0.3 * torch.randn(c, generator=g), 0.3 * torch.randn(c, generator=g)
+    check_norm(x, groups, gamma, beta, "silu", dtype, dy=dy)
