@@ -133,6 +133,21 @@ def _norm_call(n, h, w, c, pitch, groups, dtype, act, eps, grad):
     return d, int(_L().conv_group_norm_ws_bytes(d, int(grad)))
 
 
+def _pixel_pitch(x: torch.Tensor) -> int:
+    """Elements from one pixel of x to the next; 0 (the library's "c") for a
+    contiguous map."""
+    if x.is_contiguous():
+        return 0
+    # one step from pixel to pixel over the whole map: a channel slice of a wider NHWC map
+    n, h, w, c = x.shape
+    sn, sh, sw, sc = x.stride()
+    pitch = sw if w > 1 else sh if h > 1 else sn if n > 1 else c
+    # a step below c, that of a broadcast map above all, would be read as another layout
+    if (pitch < c or (c > 1 and sc != 1) or (h > 1 and sh != w * pitch) or (n > 1 and sn != h * w * pitch)):
+        raise ValueError("x must be NHWC with evenly spaced pixels (a contiguous map or a channel slice of one)")
+    return pitch
+
+
 def _norm_of(x: torch.Tensor, groups: int, eps: float, act: str, grad: bool):
     """(description, scratch bytes) of the norm of x."""
     if x.dim() != 4 or x.dtype not in _FLOATS or not x.is_cuda:
@@ -140,14 +155,7 @@ def _norm_of(x: torch.Tensor, groups: int, eps: float, act: str, grad: bool):
     if act not in NORM_ACTS:
         raise ValueError("act %r, expected one of %s" % (act, ", ".join(NORM_ACTS)))
     n, h, w, c = x.shape
-    pitch = 0
-    if not x.is_contiguous():
-        # one step from pixel to pixel over the whole map: a channel slice of a wider NHWC map
-        sn, sh, sw, sc = x.stride()
-        pitch = sw if w > 1 else sh if h > 1 else sn if n > 1 else c
-        if ((c > 1 and sc != 1) or (w > 1 and sw != pitch) or (h > 1 and sh != w * pitch) or
-                (n > 1 and sn != h * w * pitch)):
-            raise ValueError("x must be NHWC with evenly spaced pixels (a contiguous map or a channel slice of one)")
+    pitch = _pixel_pitch(x)
     return _norm_call(n, h, w, c, pitch, groups, x.dtype, act, eps, grad)
 
 

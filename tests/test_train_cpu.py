@@ -258,3 +258,30 @@ def test_group_norm_plan_covers_the_map(dtype):
                 for n, grad, align in ((1, 0, 16), (4, 1, 16), (1, 1, 2)):
                     shape = (n, 1, hw, cg * groups, groups)
                     assert norm_plan_problem(shape, dtype, align, grad) is None, (shape, grad, align)
+
+
+@pytest.mark.parametrize("x", [
+    torch.zeros(1, 1, 1, 64).expand(2, 8, 8, 64),         # one pixel for the whole map
+    torch.zeros(2, 1, 1, 64).expand(2, 8, 8, 64),
+    torch.zeros(2, 8, 1, 64).expand(2, 8, 8, 64),
+    torch.zeros(1, 8, 8, 64).expand(2, 8, 8, 64),
+    torch.zeros(1, 1, 1, 1).expand(2, 8, 8, 1),
+    torch.zeros(2, 8, 8, 1).expand(2, 8, 8, 64),
+    torch.zeros(4096).as_strided((1, 4, 4, 64), (512, 128, 32, 1)),  # pixels that overlap
+    torch.zeros(2, 64, 8, 8).permute(0, 2, 3, 1),
+    torch.zeros(2, 8, 16, 64)[:, :, :8],
+], ids=lambda t: "%s-%s" % ("x".join(map(str, t.shape)), "x".join(map(str, t.stride()))))
+def test_maps_whose_pixels_do_not_follow_each_other_are_refused(x):
+    with pytest.raises(ValueError):
+        train._pixel_pitch(x)
+
+
+@pytest.mark.parametrize("x,pitch", [
+    (torch.zeros(2, 8, 8, 64), 64), (torch.zeros(2, 8, 8, 100)[..., 20:84], 100), (torch.zeros(2, 8, 8, 5)[..., 2:3], 5),
+    (torch.zeros(2, 8, 16, 64)[:, :, ::2], 128),  # every other pixel is one step
+    (torch.zeros(1, 1, 1, 64).expand(1, 1, 1, 64), 64), (torch.zeros(1, 1, 4, 100)[..., :64], 100),
+    (torch.zeros(1, 4, 1, 100)[..., :64], 100), (torch.zeros(4, 1, 1, 100)[..., :64], 100),
+    (torch.zeros(1, 1, 1, 100)[..., :64], 64), (torch.zeros(64).as_strided((1, 1, 1, 64), (0, 0, 0, 1)), 64),
+])
+def test_pixel_pitch_of_maps_and_slices(x, pitch):
+    assert (train._pixel_pitch(x) or x.shape[3]) == pitch

@@ -635,3 +635,16 @@ def test_group_norm_of_1024_lanes_with_few_vectors(shape):
     x, dy = (torch.randn((n, h, w, c), generator=g).to(DT[dtype]) for _ in range(2))
     gamma, beta = 1 + 0.3 * torch.randn(c, generator=g), 0.3 * torch.randn(c, generator=g)
     check_norm(x, groups, gamma, beta, "silu", dtype, dy=dy)
+
+
+def test_group_norm_refuses_a_broadcast_map():
+    """One pixel's memory is not a map's: nothing is read past it."""
+    x, dy = torch.ones((1, 1, 1, 64), device="cuda").expand(2, 8, 8, 64), torch.ones((2, 8, 8, 64), device="cuda")
+    with pytest.raises(ValueError):
+        conv.group_norm(x, 4)
+    with pytest.raises(ValueError):
+        train.group_norm_ws_bytes(x, 4)
+    with pytest.raises(ValueError):
+        conv.group_norm_grad(dy, x, torch.ones((2, 4, 2), device="cuda"))
+    with pytest.raises(ValueError):
+        conv.group_norm_grad(x, dy, torch.ones((2, 4, 2), device="cuda"))
