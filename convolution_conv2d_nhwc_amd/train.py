@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+from operator import index
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -120,8 +121,10 @@ def _need(need: int, what: str) -> int:
     return need
 
 
-# The descriptions below and their scratch sizes depend on sizes and types
-# alone: they are computed once for each.
+# The descriptions below and their scratch sizes depend on sizes, types and
+# plain numbers alone: they are computed once for each. Callers convert what they
+# are given to plain numbers first: a tensor's hash is its identity, and a value
+# changed in place would find the description of the old one.
 _once = functools.lru_cache(maxsize=4096)
 
 
@@ -156,7 +159,7 @@ def _norm_of(x: torch.Tensor, groups: int, eps: float, act: str, grad: bool):
         raise ValueError("act %r, expected one of %s" % (act, ", ".join(NORM_ACTS)))
     n, h, w, c = x.shape
     pitch = _pixel_pitch(x)
-    return _norm_call(n, h, w, c, pitch, groups, x.dtype, act, eps, grad)
+    return _norm_call(n, h, w, c, pitch, index(groups), x.dtype, act, float(eps), grad)
 
 
 def _affine(gamma, beta, c):
@@ -264,7 +267,7 @@ def _head_of(x, w, labels, weights, grad):
 
 def head_loss_ws_bytes(rows: int, c: int, classes: int, grad: bool = False) -> int:
     """Bytes of ``ws`` that head_loss (or head_loss_grad) takes."""
-    return _need(_head_call(rows, c, classes, 8, bool(grad))[1], "conv_head_loss_ws_bytes")
+    return _need(_head_call(index(rows), index(c), index(classes), 8, bool(grad))[1], "conv_head_loss_ws_bytes")
 
 
 def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -331,9 +334,14 @@ def _ortho_call(batch, rows, cols, dtype, steps, a, b, c, eps):
     return d, int(_L().conv_orthogonalize_ws_bytes(d))
 
 
+def _ortho_of(batch, rows, cols, dtype, steps, a, b, c, eps):
+    """(description, scratch bytes) of the update."""
+    return _ortho_call(batch, rows, cols, dtype, index(steps), float(a), float(b), float(c), float(eps))
+
+
 def orthogonalize_ws_bytes(batch: int, rows: int, cols: int) -> int:
     """Bytes of ``ws`` that orthogonalize takes for [batch, rows, cols]."""
-    return _need(_ortho_call(batch, rows, cols, torch.float32, 1, 1.0, 0.0, 0.0, 0.0)[1],
+    return _need(_ortho_call(index(batch), index(rows), index(cols), torch.float32, 1, 1.0, 0.0, 0.0, 0.0)[1],
                  "conv_orthogonalize_ws_bytes")
 
 
@@ -352,7 +360,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = MUO
         batch, rows = 1, shape[0]
         cols = g.numel() // rows if rows else 0
     a, b, c = coeffs
-    d, need = _ortho_call(batch, rows, cols, g.dtype, steps, a, b, c, eps)
+    d, need = _ortho_of(batch, rows, cols, g.dtype, steps, a, b, c, eps)
     if out is None:
         out = torch.empty_like(g, dtype=torch.bfloat16)
     else:

@@ -285,3 +285,34 @@ def test_maps_whose_pixels_do_not_follow_each_other_are_refused(x):
 ])
 def test_pixel_pitch_of_maps_and_slices(x, pitch):
     assert (train._pixel_pitch(x) or x.shape[3]) == pitch
+
+
+class FakeMap:
+    """What _norm_of looks at of a device map."""
+    shape, dtype, is_cuda = (2, 4, 4, 16), torch.float32, True
+
+    def dim(self):
+        return 4
+
+    def is_contiguous(self):
+        return True
+
+
+def test_arguments_changed_in_place_are_read_again():
+    eps, steps, a = torch.tensor(0.25), torch.tensor(5), torch.tensor(2.0)
+    assert train._norm_of(FakeMap(), 4, eps, "none", False)[0].eps == 0.25
+    d = train._ortho_of(1, 100, 200, torch.float32, steps, a, 0.0, 0.0, eps)[0]
+    assert (d.steps, d.a, d.eps) == (5, 2.0, 0.25)
+    eps.fill_(0.5), steps.fill_(2), a.fill_(3.0)
+    assert train._norm_of(FakeMap(), 4, eps, "none", False)[0].eps == 0.5
+    d = train._ortho_of(1, 100, 200, torch.float32, steps, a, 0.0, 0.0, eps)[0]
+    assert (d.steps, d.a, d.eps) == (2, 3.0, 0.5)
+
+
+def test_sizes_are_whole_numbers_whatever_was_asked_before():
+    train._norm_of(FakeMap(), 4, 1e-5, "none", False)
+    with pytest.raises(TypeError):
+        train._norm_of(FakeMap(), 4.0, 1e-5, "none", False)
+    train._ortho_of(1, 100, 200, torch.float32, 5, 1.0, 0.0, 0.0, 1e-7)
+    with pytest.raises(TypeError):
+        train._ortho_of(1, 100, 200, torch.float32, 5.0, 1.0, 0.0, 0.0, 1e-7)
