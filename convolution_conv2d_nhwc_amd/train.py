@@ -3,10 +3,12 @@ its activation and gradients, the softmax cross entropy of a 1x1 head with
 its gradients, and the orthogonalised update of weight matrices.
 
 Argument marshalling only, as in ``_lib``: every step of the computation runs
-in the HIP library, on the current torch stream or on ``stream``. Outputs and
-scratch memory are allocated when they are not given; torch's allocator ties
-them to the current stream, so a caller that passes another ``stream`` gives
-``ws`` and the outputs too, or keeps the two streams ordered.
+in the HIP library, on the current torch stream or on ``stream`` (a torch
+stream or a HIP stream's address). A call with ``stream`` is the call under
+``torch.cuda.stream(stream)``: outputs and scratch memory that are not given
+come from that stream's memory, so they cannot be handed out again while its
+work is still to run. As under that context, the caller orders the streams that
+make the inputs and use the outputs.
 """
 from __future__ import annotations
 
@@ -108,11 +110,18 @@ def _scratch(need: int, ws: Optional[torch.Tensor], t: torch.Tensor, what: str):
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _stream(stream, t: torch.Tensor) -> int:
-    """The given stream's handle, or that of t's device's current stream."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return _lib._stream_handle(stream)
+def _on(stream, t: torch.Tensor):
+    """The context in which a call with `stream` allocates and enqueues."""
+    if not t.is_cuda:
+        raise ValueError("a call on a stream takes device tensors")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_lib._stream_handle(stream), device=t.device)
+    return torch.cuda.stream(stream)
+
+
+def _stream(t: torch.Tensor) -> int:
+    """The handle of the current stream of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _need(need: int, what: str) -> int:
@@ -184,6 +193,9 @@ def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = Non
     wider map; gamma, beta float32 [c]; act "none", "relu", "relu6", "mish"
     or "silu". stats float32 [n, groups, 2] receives (mean, 1/sqrt(var + eps)),
     which group_norm_grad takes."""
+    if stream is not None:
+        with _on(stream, x):
+            return group_norm(x, groups, gamma, beta, eps, act, y, stats, ws)
     d, need = _norm_of(x, groups, eps, act, False)
     _affine(gamma, beta, x.shape[3])
     if y is None:
@@ -194,7 +206,7 @@ def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = Non
         _dev(stats, "stats", torch.float32, (x.shape[0], groups, 2))
     ws, at, size = _scratch(need, ws, x, "conv_group_norm")
     st = _L().conv_group_norm(d, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(stats), at, size,
-                              _stream(stream, x))
+                              _stream(x))
     if st:
         _lib._check(st, "conv_group_norm")
     return y
@@ -207,6 +219,9 @@ def group_norm_grad(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gamm
     """(dx, dgamma, dbeta) of group_norm for the upstream gradient dy (x's
     shape and dtype, contiguous), from the x, gamma, beta and act of the
     forward call and the stats it wrote."""
+    if stream is not None:
+        with _on(stream, x):
+            return group_norm_grad(dy, x, stats, gamma, beta, act, dx, dgamma, dbeta, ws)
     if stats.dim() != 3:
         raise ValueError("stats must be [n, groups, 2]")
     groups = stats.shape[1]
@@ -229,7 +244,7 @@ def group_norm_grad(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gamm
         _dev(dbeta, "dbeta", torch.float32, (c,))
     ws, at, size = _scratch(need, ws, x, "conv_group_norm_grad")
     st = _L().conv_group_norm_grad(d, x.data_ptr(), dy.data_ptr(), stats.data_ptr(), _ptr(gamma), _ptr(beta),
-                                   dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), at, size, _stream(stream, x))
+                                   dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), at, size, _stream(x))
     if st:
         _lib._check(st, "conv_group_norm_grad")
     return dx, dgamma, dbeta
@@ -277,11 +292,14 @@ def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weights: O
     under the 1x1 head w [classes, c] (both bfloat16) and its weighted sum,
     or mean when weights is None, as float32. labels [...] int32 or int64; a
     pixel whose label lies outside 0 .. classes-1 is left out."""
+    if stream is not None:
+        with _on(stream, x):
+            return head_loss(x, w, labels, weights, loss, total, ws)
     d, need = _head_of(x, w, labels, weights, False)
     loss, total = _loss_outputs(x, loss, total)
     ws, at, size = _scratch(need, ws, x, "conv_head_loss")
     st = _L().conv_head_loss(d, x.data_ptr(), w.data_ptr(), labels.data_ptr(), _ptr(weights), loss.data_ptr(),
-                             total.data_ptr(), at, size, _stream(stream, x))
+                             total.data_ptr(), at, size, _stream(x))
     if st:
         _lib._check(st, "conv_head_loss")
     return total, loss
@@ -305,6 +323,9 @@ def head_loss_grad(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weigh
                    ws: Optional[torch.Tensor] = None, stream=None):
     """(total, loss, dx, dw): head_loss and the gradients of total, bfloat16
     in the shapes of x and w."""
+    if stream is not None:
+        with _on(stream, x):
+            return head_loss_grad(x, w, labels, weights, loss, total, dx, dw, ws)
     d, need = _head_of(x, w, labels, weights, True)
     loss, total = _loss_outputs(x, loss, total)
     if dx is None:
@@ -317,7 +338,7 @@ def head_loss_grad(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, weigh
         _dev(dw, "dw", w.dtype, w.shape)
     ws, at, size = _scratch(need, ws, x, "conv_head_loss_grad")
     st = _L().conv_head_loss_grad(d, x.data_ptr(), w.data_ptr(), labels.data_ptr(), _ptr(weights), loss.data_ptr(),
-                                  total.data_ptr(), dx.data_ptr(), dw.data_ptr(), at, size, _stream(stream, x))
+                                  total.data_ptr(), dx.data_ptr(), dw.data_ptr(), at, size, _stream(x))
     if st:
         _lib._check(st, "conv_head_loss_grad")
     return total, loss, dx, dw
@@ -350,6 +371,9 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = MUO
     """The Newton-Schulz orthogonalisation of g, bfloat16 in g's shape: g
     [m, n], a batch [b, m, n] of matrices, or one layer's OHWI weight gradient
     [c_out, kh, kw, c_in] as the matrix [c_out, kh kw c_in]."""
+    if stream is not None:
+        with _on(stream, g):
+            return orthogonalize(g, steps, coeffs, eps, out, ws)
     if g.dim() < 2 or g.dtype not in _FLOATS:
         raise ValueError("g must be float32 or bfloat16, [m, n], [batch, m, n] or OHWI [c_out, kh, kw, c_in]")
     shape = g.shape
@@ -366,7 +390,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = MUO
     else:
         _dev(out, "out", torch.bfloat16, shape)
     ws, at, size = _scratch(need, ws, g, "conv_orthogonalize")
-    st = _L().conv_orthogonalize(d, g.data_ptr(), out.data_ptr(), at, size, _stream(stream, g))
+    st = _L().conv_orthogonalize(d, g.data_ptr(), out.data_ptr(), at, size, _stream(g))
     if st:
         _lib._check(st, "conv_orthogonalize")
     return out

@@ -316,3 +316,15 @@ def test_sizes_are_whole_numbers_whatever_was_asked_before():
     train._ortho_of(1, 100, 200, torch.float32, 5, 1.0, 0.0, 0.0, 1e-7)
     with pytest.raises(TypeError):
         train._ortho_of(1, 100, 200, torch.float32, 5.0, 1.0, 0.0, 0.0, 1e-7)
+
+
+@pytest.mark.parametrize("call", [
+    lambda t, s: t.group_norm(torch.zeros(1, 4, 4, 8), 2, stream=s),
+    lambda t, s: t.group_norm_grad(torch.zeros(1, 4, 4, 8), torch.zeros(1, 4, 4, 8), torch.zeros(1, 2, 2), stream=s),
+    lambda t, s: t.head_loss(torch.zeros(4, 8), torch.zeros(5, 8), torch.zeros(4, dtype=torch.int64), stream=s),
+    lambda t, s: t.head_loss_grad(torch.zeros(4, 8), torch.zeros(5, 8), torch.zeros(4, dtype=torch.int64), stream=s),
+    lambda t, s: t.orthogonalize(torch.zeros(4, 8), stream=s),
+])
+def test_host_tensors_are_refused_with_a_stream_too(call):
+    with pytest.raises(ValueError):
+        call(train, 1 << 40)

@@ -648,3 +648,35 @@ def test_group_norm_refuses_a_broadcast_map():
         conv.group_norm_grad(dy, x, torch.ones((2, 4, 2), device="cuda"))
     with pytest.raises(ValueError):
         conv.group_norm_grad(x, dy, torch.ones((2, 4, 2), device="cuda"))
+
+
+@pytest.mark.parametrize("form", ["stream", "address"])
+def test_memory_of_a_call_with_a_stream_is_that_streams(form, monkeypatch):
+    """Outputs and scratch that the wrapper allocates belong to the stream that
+    uses them, wherever the caller is; results are those of the current stream."""
+    d, _ = all_calls(6)
+    stats = torch.empty((1, 4, 2), device="cuda")
+    calls = [lambda **k: conv.group_norm(d["x2"], 4, act="mish", stats=stats, **k),
+             lambda **k: conv.group_norm_grad(d["dy2"], d["x2"], stats, act="mish", **k),
+             lambda **k: conv.head_loss(d["bx"], d["bw"], d["bl"], **k),
+             lambda **k: conv.head_loss_grad(d["bx"], d["bw"], d["bl"], **k),
+             lambda **k: conv.orthogonalize(d["g2"], **k)]
+    flat = lambda r: list(r) if isinstance(r, tuple) else [r]  # noqa: E731
+    want = [[t.clone() for t in flat(c())] for c in calls]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    seen = []
+    for name in ("empty", "empty_like"):
+        def spy(*a, _real=getattr(torch, name), **k):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+            return _real(*a, **k)
+        monkeypatch.setattr(torch, name, spy)
+    here = torch.cuda.current_stream()
+    for call, ref in zip(calls, want):
+        seen.clear()
+        got = flat(call(stream=side if form == "stream" else side.cuda_stream))
+        assert seen and set(seen) == {side.cuda_stream}
+        assert torch.cuda.current_stream() == here
+        side.synchronize()
+        for a, b in zip(got, ref):
+            assert torch.equal(a, b)
