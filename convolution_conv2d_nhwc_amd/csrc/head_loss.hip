@@ -599,6 +599,10 @@ static int logits_tile(int64_t classes, int64_t rows, int64_t c) {
   return t == 256 && c <= 256 ? 128 : t;
 }
 
+int64_t head_workgroups(const conv_head_desc& d) {
+  return gemm_tiles(d.classes, d.rows, logits_tile(d.classes, d.rows, d.c), false);
+}
+
 HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w) {
   HeadPlan p = {};
   const int64_t rows = d.rows, c = d.c, v = d.classes;

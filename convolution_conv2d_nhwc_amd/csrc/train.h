@@ -89,6 +89,8 @@ struct HeadArgs {
   HeadPlan p;
 };
 
+// Workgroups of the logits' product, the widest launch.
+int64_t head_workgroups(const conv_head_desc& d);
 // copy_x, copy_w: the operand cannot be read in place (c % 8 or alignment).
 HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w);
 hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s);

@@ -89,6 +89,8 @@ conv_status head_check(const conv_head_desc* d) {
   if (d->c > 65536 || d->rows > (1 << 22) - 64 || d->classes > (1 << 22) - 64) return CONV_E_UNSUPPORTED;
   const int64_t c = (d->c + 7) / 8 * 8, most = (std::max(d->rows, d->classes) + 63) / 64 * 64;
   if (most * c * 2 >= kMaxBytes) return CONV_E_UNSUPPORTED;
+  // a launch has fewer than 2^32 lanes, 256 a workgroup
+  if (head_workgroups(*d) >= 1 << 24) return CONV_E_UNSUPPORTED;
   return CONV_OK;
 }
 

@@ -111,8 +111,8 @@ int64_t conv_head_loss_ws_bytes(const conv_head_desc* d, int32_t grad);
  * Logits, sums and losses in fp32 from the bf16 products. Alignment: x, w to
  * 2 bytes (16 with c % 8 == 0 is read in place, otherwise through a copy in
  * ws), ws to 256. CONV_E_SHAPE: a size <= 0. CONV_E_UNSUPPORTED: dtype,
- * label_bytes, c over 65536, rows or classes over 2^22 - 64, or a size
- * limit. */
+ * label_bytes, c over 65536, rows or classes over 2^22 - 64, 2^24 tiles of
+ * logits or more (128 x 128, or 256 x 256 above 256 channels), or a size limit. */
 conv_status conv_head_loss(const conv_head_desc* d, const void* x, const void* w, const void* labels,
                            const float* weights, float* loss, float* total, void* ws, int64_t ws_bytes,
                            void* stream);

@@ -328,3 +328,19 @@ def test_sizes_are_whole_numbers_whatever_was_asked_before():
 def test_host_tensors_are_refused_with_a_stream_too(call):
     with pytest.raises(ValueError):
         call(train, 1 << 40)
+
+
+@pytest.mark.parametrize("rows,classes,c,ok", [
+    (1 << 20, 1 << 18, 8, False), ((1 << 20) - 128, 1 << 18, 8, True), (1 << 18, 1 << 20, 200, False),
+    (1 << 20, 1 << 18, 264, True), (1 << 21, 1 << 19, 264, False), ((1 << 21) - 256, 1 << 19, 264, True),
+    ((1 << 22) - 64, (1 << 22) - 64, 8, False),
+])
+def test_head_loss_refuses_more_workgroups_than_a_launch_has(rows, classes, c, ok):
+    """256 lanes a workgroup, fewer than 2^32 a launch: refused by name, not by
+    the launch after others are already enqueued."""
+    d = head_desc(rows=rows, classes=classes, c=c)
+    for grad in (0, 1):
+        need = train._L().conv_head_loss_ws_bytes(d, grad)
+        assert need > 0 if ok else need == E_UNSUPPORTED
+        if not ok:
+            assert head(d, A, grad) == E_UNSUPPORTED
