@@ -763,11 +763,15 @@ inline int gemm_tile(int64_t q, int64_t p, int64_t others, bool symmetric) {
                                                             : 64;
 }
 
-// Deep: as many workgroups as CUs or fewer have a CU's LDS each.
+// Deep: as many workgroups as CUs or fewer have a CU's LDS each. A 256 tile always has.
+inline bool gemm_deep(int64_t q, int64_t p, int tile, int64_t others, bool symmetric) {
+  return tile == 256 || gemm_tiles(q, p, tile, symmetric) * others <= 256;
+}
+
 template <int DT, bool KSA, bool KSB, class Epi>
 hipError_t gemm_launch(const GemmArgs& g, const typename Epi::Args& e, int tile, int splits, int batch,
                        hipStream_t s) {
-  const bool deep = gemm_tiles(g.q, g.p, tile, Epi::kSymmetric) * splits * batch <= 256;
+  const bool deep = gemm_deep(g.q, g.p, tile, (int64_t)splits * batch, Epi::kSymmetric);
   switch (tile) {
     case 256: return gemm_launch_t<DT, 256, true, KSA, KSB, Epi>(g, e, splits, batch, s);
     case 128:

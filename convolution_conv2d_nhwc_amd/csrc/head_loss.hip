@@ -30,6 +30,8 @@
 // results, nearly all of it from the one large entry of a row, its label's.
 // What that rounding left out, delta[r], is kept in fp32 and put back: in dx as
 // delta[r] w[label] in the epilogue, in dw as the product's sparse term.
+#include <cstdio>
+
 #include "gemm.h"
 #include "train.h"
 
@@ -644,6 +646,21 @@ HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w)
   }
   p.bytes = at;
   return p;
+}
+
+void head_describe(const conv_head_desc& d, bool grad, const HeadPlan& p, char* buf, int len) {
+  auto per_cu = [](int64_t q, int64_t r, const GemmShape& g) { return gemm_deep(q, r, g.tile, g.splits, false) ? 1 : 2; };
+  const int n = std::snprintf(buf, len, "head_loss%s logits=%dx%d slots=%d finish=%d copy_x=%d copy_w=%d",
+                              grad ? "_grad" : "", p.stat_tile, per_cu(d.classes, d.rows, {p.stat_tile, 1}), p.slots,
+                              d.rows <= kFinishRows && p.slots <= kFinishSlots ? 1 : 2, p.copy_x, p.o_w >= 0);
+  if (!grad || n < 0 || n >= len) return;
+  const int64_t pv = std::min(p.vp, d.classes);
+  // a pair's products share a launch built for one workgroup a CU
+  const int dx = p.pair ? 1 : per_cu(p.cpad, d.rows, p.dx), dw = p.pair ? 1 : per_cu(p.cpad, up(pv, 8), p.dw);
+  std::snprintf(buf + n, len - n,
+                " pieces=%d g=%dx%d pair=%d dx=%dx%d dx_splits=%d dx_part=%d dw=%dx%d dw_splits=%d dw_part=%d",
+                cdiv(d.classes, p.vp), p.ds_tile, per_cu(pv, d.rows, {p.ds_tile, 1}), p.pair, p.dx.tile, dx,
+                p.dx.splits, p.o_dxp >= 0, p.dw.tile, dw, p.dw.splits, p.o_dwp >= 0);
 }
 
 namespace {

@@ -26,6 +26,8 @@
 // zero. What bounds it: the matrix cores at large sizes; at small ones the
 // 3 steps + 2 launches. 1024 x 4608 in five steps: 255 us, a step 18 (A) + 9 (Q)
 // + 22 (Q X), and 14 before the first; six of 250 x 1000: 122 us.
+#include <cstdio>
+
 #include "gemm.h"
 #include "train.h"
 
@@ -700,6 +702,22 @@ void launch_small(const OrthoArgs& a, const Layout& l, int out_vec, hipStream_t 
 
 int64_t ortho_ws_bytes(const conv_ortho_desc& d) { return ortho_layout(d.batch, layout_of(d.rows, d.cols)).bytes; }
 
+// Tiles of the symmetric products and of the step's.
+static int sym_tile_of(const Layout& l, int64_t batch) { return gemm_tile(l.mp, l.mp, batch, true); }
+static int step_tile_of(const Layout& l, int64_t batch) { return gemm_tile(l.np, l.mp, batch, false); }
+
+void ortho_describe(const conv_ortho_desc& d, char* buf, int len) {
+  const Layout l = layout_of(d.rows, d.cols);
+  if (!ortho_layout(d.batch, l).bytes) {
+    std::snprintf(buf, len, "ortho small m=%d n=%d tall=%d blocks=%d", l.m, l.n, l.tall, cdiv(l.np, 16 * kSmallWaves));
+    return;
+  }
+  const int sym = sym_tile_of(l, d.batch), step = step_tile_of(l, d.batch);
+  std::snprintf(buf, len, "ortho m=%d n=%d tall=%d sym=%dx%d step=%dx%d", l.m, l.n, l.tall, sym,
+                gemm_deep(l.mp, l.mp, sym, d.batch, true) ? 1 : 2, step,
+                gemm_deep(l.np, l.mp, step, d.batch, false) ? 1 : 2);
+}
+
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   const Layout l = layout_of(a.rows, a.cols);
   const int out_row = l.tall ? l.m : l.n;
@@ -720,8 +738,7 @@ hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s) {
   _Float16* r = reinterpret_cast<_Float16*>(a.ws + w.r);
   float* d = reinterpret_cast<float*>(a.ws + w.d);
   float* e = reinterpret_cast<float*>(a.ws + w.e);
-  const int sym_tile = gemm_tile(l.mp, l.mp, a.batch, true);
-  const int step_tile = gemm_tile(l.np, l.mp, a.batch, false);
+  const int sym_tile = sym_tile_of(l, a.batch), step_tile = step_tile_of(l, a.batch);
   for (int k = 0; k < a.steps; ++k) {
     const bool last = k + 1 == a.steps;
     _Float16* hi = reinterpret_cast<_Float16*>(a.ws + (k % 2 ? w.hi1 : w.hi0));

@@ -93,6 +93,8 @@ struct HeadArgs {
 int64_t head_workgroups(const conv_head_desc& d);
 // copy_x, copy_w: the operand cannot be read in place (c % 8 or alignment).
 HeadPlan head_plan(const conv_head_desc& d, bool grad, bool copy_x, bool copy_w);
+// The plan in words: each product's tile side x workgroups a CU, and its splits.
+void head_describe(const conv_head_desc& d, bool grad, const HeadPlan& p, char* buf, int len);
 hipError_t launch_head_loss(const HeadArgs& a, bool grad, hipStream_t s);
 
 // ---- orthogonalisation ----------------------------------------------------------
@@ -108,6 +110,7 @@ struct OrthoArgs {
 };
 
 int64_t ortho_ws_bytes(const conv_ortho_desc& d);
+void ortho_describe(const conv_ortho_desc& d, char* buf, int len);
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s);
 
 }  // namespace convnhwc

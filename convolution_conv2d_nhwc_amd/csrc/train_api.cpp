@@ -154,6 +154,15 @@ int64_t conv_head_loss_ws_bytes(const conv_head_desc* d, int32_t grad) {
   return st != CONV_OK ? (int64_t)st : head_plan(*d, grad != 0, true, true).bytes;
 }
 
+conv_status conv_head_loss_describe(const conv_head_desc* d, int32_t grad, int32_t align, char* buf, int32_t len) {
+  if (!d || !buf || len <= 0) return CONV_E_NULL;
+  const conv_status st = head_check(d);
+  if (st != CONV_OK) return st;
+  const bool copy = d->c % 8 || align % 16;
+  head_describe(*d, grad != 0, head_plan(*d, grad != 0, copy, copy), buf, len);
+  return CONV_OK;
+}
+
 conv_status conv_head_loss(const conv_head_desc* d, const void* x, const void* w, const void* labels,
                            const float* weights, float* loss, float* total, void* ws, int64_t ws_bytes,
                            void* stream) {
@@ -169,6 +178,14 @@ conv_status conv_head_loss_grad(const conv_head_desc* d, const void* x, const vo
 int64_t conv_orthogonalize_ws_bytes(const conv_ortho_desc* d) {
   const conv_status st = ortho_check(d);
   return st != CONV_OK ? (int64_t)st : ortho_ws_bytes(*d);
+}
+
+conv_status conv_orthogonalize_describe(const conv_ortho_desc* d, char* buf, int32_t len) {
+  if (!d || !buf || len <= 0) return CONV_E_NULL;
+  const conv_status st = ortho_check(d);
+  if (st != CONV_OK) return st;
+  ortho_describe(*d, buf, len);
+  return CONV_OK;
 }
 
 conv_status conv_orthogonalize(const conv_ortho_desc* d, const void* g, void* out, void* ws, int64_t ws_bytes,

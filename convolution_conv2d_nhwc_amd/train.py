@@ -63,12 +63,16 @@ def _L():
         HD, OD = ctypes.POINTER(_HeadDesc), ctypes.POINTER(_OrthoDesc)
         L.conv_head_loss_ws_bytes.argtypes = [HD, I32]
         L.conv_head_loss_ws_bytes.restype = I64
+        L.conv_head_loss_describe.argtypes = [HD, I32, I32, ctypes.c_char_p, I32]
+        L.conv_head_loss_describe.restype = ctypes.c_int
         L.conv_head_loss.argtypes = [HD] + [P] * 7 + [I64, P]
         L.conv_head_loss.restype = ctypes.c_int
         L.conv_head_loss_grad.argtypes = [HD] + [P] * 9 + [I64, P]
         L.conv_head_loss_grad.restype = ctypes.c_int
         L.conv_orthogonalize_ws_bytes.argtypes = [OD]
         L.conv_orthogonalize_ws_bytes.restype = I64
+        L.conv_orthogonalize_describe.argtypes = [OD, ctypes.c_char_p, I32]
+        L.conv_orthogonalize_describe.restype = ctypes.c_int
         L.conv_orthogonalize.argtypes = [OD, P, P, P, I64, P]
         L.conv_orthogonalize.restype = ctypes.c_int
         _bound = L

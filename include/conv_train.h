@@ -102,6 +102,9 @@ typedef struct conv_head_desc {
 /* Scratch of conv_head_loss (grad = 0) or conv_head_loss_grad (grad = 1). */
 int64_t conv_head_loss_ws_bytes(const conv_head_desc* d, int32_t grad);
 
+/* The products' tiles for x and w of the given common alignment, as conv_describe. */
+conv_status conv_head_loss_describe(const conv_head_desc* d, int32_t grad, int32_t align, char* buf, int32_t len);
+
 /*   x       : device [rows][c] (an NHWC map)
  *   w       : device [classes][c] (OHWI of a 1x1 layer)
  *   labels  : device int32 or int64 [rows]
@@ -142,6 +145,9 @@ typedef struct conv_ortho_desc {
 } conv_ortho_desc;
 
 int64_t conv_orthogonalize_ws_bytes(const conv_ortho_desc* d);
+
+/* The kernels and tiles it takes, as conv_describe. */
+conv_status conv_orthogonalize_describe(const conv_ortho_desc* d, char* buf, int32_t len);
 
 /*   g   : device [batch][rows][cols] of dtype
  *   out : device [batch][rows][cols] bf16 (one RNE rounding)

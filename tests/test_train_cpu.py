@@ -13,6 +13,7 @@ pytestmark = pytest.mark.skipif(not os.path.exists(_lib.library_path()), reason=
 
 if os.path.exists(_lib.library_path()):
     from convolution_conv2d_nhwc_amd import train
+    from tests.train_cases import LOSS_TILES, ORTHO_TILES, described, loss_kernels, ortho_kernels
 
 E_NULL, E_SHAPE, E_UNSUPPORTED, E_ALIGN, E_ALIAS, E_SCRATCH = -1, -2, -3, -4, -5, -8
 A = [(i + 1) << 36 for i in range(12)]  # addresses far apart
@@ -207,13 +208,6 @@ def test_ws_bytes_from_python_raise_named_errors():
     assert train.head_loss_ws_bytes(100, 64, 1000, grad=True) > train.head_loss_ws_bytes(100, 64, 1000) > 0
 
 
-def described(call, *args):
-    """The key=value fields of a describe entry point's text."""
-    buf = ctypes.create_string_buffer(256)
-    assert call(*args, buf, 256) == 0
-    return {k: int(v) if v.isdigit() else v for k, v in (f.split("=") for f in buf.value.decode().split() if "=" in f)}
-
-
 # n, h, w, c, groups, dtype: maps whose tile needs 3 or 4 vectors of 1024 lanes but over 8 of 512
 ODD_LANES = [(1, 18, 25, 72, 1, 1), (4, 15, 30, 576, 8, 1), (1, 14, 15, 76, 4, 1), (1, 11, 14, 104, 1, 0),
              (16, 17, 17, 448, 32, 0), (1, 3, 3, 301, 1, 0)]
@@ -344,3 +338,32 @@ def test_head_loss_refuses_more_workgroups_than_a_launch_has(rows, classes, c, o
         assert need > 0 if ok else need == E_UNSUPPORTED
         if not ok:
             assert head(d, A, grad) == E_UNSUPPORTED
+
+
+TILES = ["64x1", "64x2", "128x1", "128x2", "256x1"]  # side x workgroups a CU
+
+
+def test_every_product_of_the_head_loss_has_a_case():
+    """The GPU tests' sizes reach each kernel that the rules can choose."""
+    got = set().union(*(loss_kernels(*s) for s in LOSS_TILES + [(125, 64, 1000)]))
+    want = {(p, t) for p in ("logits", "g") for t in TILES}
+    want |= {(p, t, part) for p in ("dx", "dw") for t in TILES for part in (0, 1)}
+    want |= {("pair",), ("pieces", "256x1")}
+    assert not want - got, sorted(want - got)
+
+
+def test_every_product_of_the_update_has_a_case():
+    small = [(1, 64, n) for n in (256, 512, 768, 1024)]
+    got = set().union(*(ortho_kernels(*s) for s in ORTHO_TILES + small))
+    want = {(p, t) for p in ("sym", "step") for t in TILES} | {("small", b) for b in (1, 2, 3, 4)}
+    assert not want - got, sorted(want - got)
+
+
+def test_describe_refuses_as_the_calls_do():
+    L, buf = train._L(), ctypes.create_string_buffer(512)
+    for call, good, bad in ((lambda *a: L.conv_group_norm_describe(a[0], 0, 16, *a[1:]), norm_desc(), norm_desc(c=0)),
+                            (lambda *a: L.conv_head_loss_describe(a[0], 1, 16, *a[1:]), head_desc(), head_desc(c=0)),
+                            (L.conv_orthogonalize_describe, ortho_desc(), ortho_desc(rows=0))):
+        assert call(None, buf, 512) == E_NULL and call(good, None, 512) == E_NULL and call(good, buf, 0) == E_NULL
+        assert call(bad, buf, 512) == E_SHAPE
+        assert call(good, buf, 8) == 0 and len(buf.value) == 7  # cut to the buffer
