@@ -755,8 +755,16 @@ hipError_t gemm_launch_pair(GemmArgs g0, const typename P0::Epi::Args& e0, GemmA
   return hipGetLastError();
 }
 
-// Tile: 256 when that fills the chip (one workgroup a CU), else 128 when it
-// gives at least half a chip, else 64.
+// Tile: 256 from 192 workgroups on (one a CU, three quarters of the CUs), else 128
+// from 128 on, else 64. A wider tile reads less and has fewer workgroups. Head
+// loss forward, 1024 channels, 4096 classes: 2816 rows (176 tiles of 256, 704 of
+// 128) 36 us in 256 tiles, 34 in 128; 3200 rows (208 of 256) 37 and 40; 1024 rows
+// (256 of 128, 1024 of 64) 20 us in 128 tiles, 24 in 64; below that the two are level
+// up to 1024 channels. Update's symmetric products: 2048 x 4608 (136 of 128) 581 us a
+// call in 128 tiles, 702 in 64; 1024 x 4608 (36 of 128) 358 and 249. Where most of
+// a tile is padding or the 256 tiles are few over a round the rule is off: six
+// matrices of 260 x 4608 take 316 us with steps in 256 tiles (216 of them, a third
+// padding), 253 in 128; two of 2048 x 4608 (288) 1232 and 1023.
 inline int gemm_tile(int64_t q, int64_t p, int64_t others, bool symmetric) {
   return gemm_tiles(q, p, 256, symmetric) * others >= 192   ? 256
          : gemm_tiles(q, p, 128, symmetric) * others >= 128 ? 128

@@ -22,8 +22,14 @@
 // streaming its share of the pixels a block ahead of its arithmetic; the second
 // read comes from the last-level cache as far as the map fits there. 16 x 160 x
 // 160 x 128 bf16: 20 us for the statistics (5.1 TB/s), 39 to apply them
-// (5.4 TB/s), 73 as a call over inputs that the cache does not hold; 20 x 20 x
-// 512 in one launch 7 us.
+// (5.4 TB/s); over inputs that the cache does not hold 30 + 43, 73 as a call. 20 x
+// 20 x 512 in one launch 7 us.
+//
+// Registers: 1024 lanes leave 128 each, so the one-launch gradient of eight
+// bf16 a vector keeps 23 of its values in scratch memory, 51 where vectors straddle
+// groups (16 x 30 x 30 x 256: 27 us, 0.8 TB/s; 22 x 22 in 512 lanes 11 us, 1.1 TB/s),
+// and so does the streamed gradient of straddling vectors, 19 and 33 (16 x 80 x
+// 80 x 80 in 8 groups: 16 + 25 us; 96 channels, where none straddles, 15 + 17).
 #include <algorithm>
 
 #include "device_common.h"

@@ -401,7 +401,9 @@ Layout layout_of(int64_t rows, int64_t cols) {
 // registers: 64 x 576 takes 30 us against 78 in 17 launches. X lives in fp32
 // in the lanes that compute it (up to four blocks of 16 columns a wave, in the
 // MFMA result's layout: p = lane % 16 of four row blocks, four consecutive
-// columns) and in fp16 in LDS for the products; O and R as above. Of A and A A
+// columns; a fourth block, above 768 columns, leaves 22 registers in scratch memory:
+// 64 x 768 takes 36 us, 64 x 1024 48) and in fp16 in LDS for the products; O and
+// R as above. Of A and A A
 // ten waves compute one 16 x 16 block of the lower triangle each and store
 // both halves. Rows in LDS are 16 bytes longer than their values, so that the 16
 // rows of one read fall on different banks.

@@ -9,6 +9,10 @@ stream or a HIP stream's address). A call with ``stream`` is the call under
 come from that stream's memory, so they cannot be handed out again while its
 work is still to run. As under that context, the caller orders the streams that
 make the inputs and use the outputs.
+
+Nothing here is recorded by autograd: a tensor that requires a gradient is read
+like any other and the results carry no graph. The gradients are the *_grad
+functions' results.
 """
 from __future__ import annotations
 
